@@ -1,0 +1,131 @@
+/*
+ * libfp8gemm — rows that are routed to one of many weights: what stands
+ * between a mixture-of-experts layer's tokens and the grouped products of
+ * fp8gemm.h (the router's choice, the rows' order, the copies to the experts'
+ * rows and the weighted sums back, each with its gradient), and a shared
+ * projection with a low-rank adapter per row.
+ *
+ * The conventions of fp8gemm.h hold for every call: device pointers owned by
+ * the caller, row-major tensors without padding, asynchronous on `stream`, no
+ * synchronisation and no allocation (the adapter products share the split-K
+ * workspace of the dense calls, by the same rules), argument errors reported
+ * before anything is launched, deterministic results.  Values in device index
+ * arrays are never checked on the host; those out of range have the meanings
+ * given per call and never lead to an access out of bounds.
+ */
+#ifndef FP8GEMM_ROUTED_H
+#define FP8GEMM_ROUTED_H
+
+#include <stdint.h>
+
+#include "fp8gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/*
+ * The router's choice.  logits [T,E] (fp32, or bf16 bits); for each token the
+ * k greatest logits in descending order, ties to the lowest index:
+ *   ids [T,k] (int32), w [T,k] (fp32).
+ * A logit of -inf or NaN is no choice: its expert is never taken and has no
+ * share in the softmax.  With p the softmax of the token's other logits,
+ *   w[t,j] = scale * p[ids[t,j]]                         (renorm == 0)
+ *   w[t,j] = scale * p[ids[t,j]] / sum_i p[ids[t,i]]     (renorm != 0);
+ * several logits of +inf share the whole weight equally.  Where fewer than k
+ * experts can be taken, the last choices are id -1 with weight 0.
+ * Constraints: 1 <= k <= min(E, 64), E <= 1024, scale finite and > 0; logits
+ * 16-byte aligned, the others 4-byte.  T == 0 returns FP8GEMM_OK.
+ */
+int moe_topk_f32(const float *logits, int32_t *ids, float *w, int T, int E, int k, int renorm,
+                 float scale, void *stream);
+int moe_topk_bf16(const void *logits, int32_t *ids, float *w, int T, int E, int k, int renorm,
+                  float scale, void *stream);
+
+/*
+ * Its gradient: dlogits [T,E] (the logits' type, every element written) from
+ * dw [T,k] and the call's logits, ids and w:
+ *   renorm != 0: dlogits[ids[j]] = w[j] (dw[j] - sum_i w[i] dw[i] / scale), 0 elsewhere
+ *   renorm == 0: dlogits[e] = [e = ids[j]] w[j] dw[j] - p[e] sum_i w[i] dw[i].
+ * dw beside an id outside [0,E) is not used.  Constraints as above; dlogits
+ * 16-byte aligned.
+ */
+int moe_topk_backward_f32(const float *logits, const int32_t *ids, const float *w, const float *dw,
+                          float *dlogits, int T, int E, int k, int renorm, float scale,
+                          void *stream);
+int moe_topk_backward_bf16(const void *logits, const int32_t *ids, const float *w, const float *dw,
+                           void *dlogits, int T, int E, int k, int renorm, float scale,
+                           void *stream);
+
+/*
+ * Choices sorted by expert, for the layouts of the grouped products.
+ * ids [S] (int32) are the choices of all tokens, token by token (S = T k);
+ * a value outside [0,G) belongs to no expert here.  row [S] gets each
+ * choice's row in the experts' operand, -1 if it has none; the choices of one
+ * expert keep their order.
+ *
+ * Contiguous: expert g's rows start at the sum of the earlier experts' counts,
+ * each rounded up to 128 rows.  m_indices [M] (every element written) names
+ * each row's expert, -1 on padding, as grouped_contiguous reads it;
+ * counts [G] gets the experts' choices.  M % 128 == 0;
+ * moe_contiguous_rows(S, G) rows hold any ids, and choices whose row would be
+ * past M get -1.
+ * Masked: expert g's rows start at g * M (M its capacity); choices past M get
+ * -1, and masked_m [G] = min(count, M), as grouped_masked reads it.
+ *
+ * ws: moe_sort_workspace(S, G) int32 of the caller's, contents arbitrary, free
+ * again when the call's work is done (may be NULL when that is 0).
+ * Constraints: S >= 0, 1 <= G <= 1024, M >= 0; S + 127 G (masked: S + G M)
+ * below 2^31 - 4096; pointers 4-byte aligned.
+ */
+int moe_contiguous_rows(int S, int G);
+int moe_sort_workspace(int S, int G);
+int moe_sort_contiguous(const int32_t *ids, int32_t *row, int32_t *m_indices, int32_t *counts,
+                        int32_t *ws, int S, int G, int M, void *stream);
+int moe_sort_masked(const int32_t *ids, int32_t *row, int32_t *masked_m, int32_t *ws, int S, int G,
+                    int M, void *stream);
+
+/*
+ * Tokens copied to their experts' rows: X [T,H] (bf16), row [T,k] as the sort
+ * gives it, A [G][M,H] (contiguous layout: G = 1).  Each token's row goes to
+ * its k rows; a row value outside [0, G M) is skipped; rows that no choice
+ * names keep their previous contents.  Two choices must not name one row.
+ *   moe_dispatch_bf16: the bf16 row itself.
+ *   moe_dispatch_fp8: its 1x128 quantisation, the codes and scales that
+ *     quantize_fp8_1x128 gives, bit for bit: A [G][M,H] codes,
+ *     sa [G][H/128][M].  H % 128 == 0.
+ * Constraints: k >= 1; T k, G M and T below 2^31 (tensors may be larger than
+ * 2^31 bytes); X and A 16-byte aligned, sa and row 4-byte.  T == 0 or H == 0
+ * returns FP8GEMM_OK.
+ */
+int moe_dispatch_bf16(const void *X, const int32_t *row, void *A, int T, int H, int k, int M, int G,
+                      void *stream);
+int moe_dispatch_fp8(const void *X, const int32_t *row, void *A, float *sa, int T, int H, int k,
+                     int M, int G, void *stream);
+
+/*
+ * Rows summed back to tokens: Y [M,H] (bf16; the masked layout's G M rows
+ * count as M here), row [T,k], w [T,k] (fp32, or NULL for weights of 1),
+ *   out[t] = sum_j w[t,j] Y[row[t,j]]    (bf16, every element written)
+ * in fp32, j ascending, one rounding at the end.  A row value outside [0,M)
+ * adds nothing, whatever its weight.  With w == NULL this is the gradient of
+ * moe_dispatch_* (the quantisation's passed straight through).
+ */
+int moe_combine_bf16(const void *Y, const int32_t *row, const float *w, void *out, int T, int H,
+                     int k, int M, void *stream);
+
+/*
+ * Its gradients, from dout [T,H] (bf16): dY[row[t,j]] = w[t,j] dout[t] (bf16;
+ * rows that no choice names keep their previous contents) and
+ * dw[t,j] = sum_h dout[t,h] Y[row[t,j],h] (fp32; 0 where row[t,j] is outside
+ * [0,M)).  Constraints of both: k >= 1; T k, M below 2^31; dout, Y, dY and out
+ * 16-byte aligned, the others 4-byte; dY is not Y.
+ */
+int moe_combine_backward_bf16(const void *dout, const void *Y, const int32_t *row, const float *w,
+                              void *dY, float *dw, int T, int H, int k, int M, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* FP8GEMM_ROUTED_H */

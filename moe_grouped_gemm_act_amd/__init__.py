@@ -349,3 +349,9 @@ def grouped_masked_bf16(A, B, masked_m, expected_m, D=None, stream=None):
     _check(load_library().grouped_masked_bf16(_p(A), _p(B), _p(D), M, N, K, G,
                                               _stream(stream, dev), _p(masked_m), int(expected_m)))
     return D
+
+
+from . import routed as _routed  # noqa: E402  (uses the helpers above)
+from .routed import *  # noqa: E402,F401,F403
+
+__all__ += _routed.__all__

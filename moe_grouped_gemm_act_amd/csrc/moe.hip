@@ -1,0 +1,687 @@
+// Routing of a mixture-of-experts layer for gfx950: the router's top-k choice
+// and softmax weights, the choices sorted by expert, tokens copied to their
+// experts' rows (bf16, or quantised 1x128 to FP8) and the rows summed back to
+// tokens, with their gradients.  Everything here is bound by memory or, for
+// the small calls of a decode step, by launch and load latency.
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "bf16.h"
+#include "e4m3.h"
+#include "fp8gemm_routed.h"
+
+namespace {
+
+constexpr long long LIM = 1LL << 31;
+
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
+
+// the launch's own status (hipGetLastError would also report an earlier call's)
+int launch(const void *f, dim3 grid, dim3 block, void **args, void *stream) {
+  return hipLaunchKernel(f, grid, block, args, 0, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? FP8GEMM_OK
+             : FP8GEMM_LAUNCH_FAILED;
+}
+
+// ---- the router's choice ---------------------------------------------------
+// Logits as unsigned keys in the order of their values (-0 and +0 alike); 0
+// for those that are no choice (NaN, -inf).  The key of every other value is
+// above that of -inf.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t u = __float_as_uint(x + 0.f);  // -0 -> +0
+  const uint32_t key = u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+  return (x > -__builtin_inff()) ? key : 0u;  // false for NaN
+}
+__device__ __forceinline__ float value_of(uint32_t key) {
+  return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+// exp(x - m) for the greatest value m: 1 where x is m, so several infinities
+// share the weight; 0 for values that are no choice
+__device__ __forceinline__ float weight_of(uint32_t key, float m) {
+  const float x = value_of(key);
+  return key == 0 ? 0.f : x == m ? 1.f : expf(x - m);
+}
+
+// V consecutive logits of one token from element e0 (the rest of a row past E: no choice)
+template <int V, bool BF>
+__device__ __forceinline__ void load_logits(const void *logits, size_t at, int e0, int E,
+                                            uint32_t (&key)[V]) {
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    float x = -__builtin_inff();
+    if (e0 + i < E)
+      x = BF ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(logits)[at + e0 + i] << 16)
+             : static_cast<const float *>(logits)[at + e0 + i];
+    key[i] = key_of(x);
+  }
+}
+
+// One wave per token, V consecutive logits per lane (E <= 64 V).  Each of the
+// k rounds takes the wave's greatest key; the first lane that holds it, and in
+// that lane the first such element, is the lowest index.
+template <int V, bool BF>
+__global__ __launch_bounds__(256) void topk_kernel(const void *logits, int32_t *ids, float *w, int T,
+                                                   int E, int k, int renorm, float scale) {
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;
+  uint32_t key[V];
+  load_logits<V, BF>(logits, (size_t)t * E, lane * V, E, key);
+  float m = 0.f, sum = 0.f, mine = 0.f;
+  int id = -1;
+  if (!renorm) {
+    uint32_t best = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) best = max(best, key[i]);
+    m = value_of(wave_max(best));
+#pragma unroll
+    for (int i = 0; i < V; ++i) sum += weight_of(key[i], m);
+    sum = wave_sum(sum);
+  }
+  for (int j = 0; j < k; ++j) {
+    uint32_t best = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < V; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
+      }
+    const uint32_t top = wave_max(best);
+    if (top == 0) break;  // no choice is left
+    if (j == 0) m = value_of(top);
+    const int from = __builtin_ctzll(__ballot(best == top));
+    const float p = weight_of(top, m);
+    if (renorm) sum += p;
+    const int e = from * V + (int)lane_of(at, from);
+    if (lane == j) {
+      id = e;
+      mine = p;
+    }
+    if (lane == from) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (i == at) key[i] = 0;
+    }
+  }
+  if (lane < k) {
+    ids[(size_t)t * k + lane] = id;
+    w[(size_t)t * k + lane] = id < 0 ? 0.f : scale * (mine / sum);
+  }
+}
+
+template <int V, bool BF>
+__global__ __launch_bounds__(256) void topk_backward_kernel(const void *logits, const int32_t *ids,
+                                                            const float *w, const float *dw,
+                                                            void *dlogits, int T, int E, int k,
+                                                            int renorm, float scale) {
+  const int lane = threadIdx.x & 63;
+  const int t = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;
+  int id = -1;
+  float g = 0.f, wj = 0.f;
+  if (lane < k) {
+    id = ids[(size_t)t * k + lane];
+    if (id < 0 || id >= E) id = -1;
+    if (id >= 0) {
+      wj = w[(size_t)t * k + lane];
+      g = dw[(size_t)t * k + lane];
+    }
+  }
+  const float mean = wave_sum(wj * g);
+  float p[V];
+  if (renorm) {
+    g = wj * (g - mean / scale);
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = 0.f;
+  } else {
+    g = wj * g;
+    uint32_t key[V], best = 0;
+    load_logits<V, BF>(logits, (size_t)t * E, lane * V, E, key);
+#pragma unroll
+    for (int i = 0; i < V; ++i) best = max(best, key[i]);
+    const float m = value_of(wave_max(best));
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      p[i] = weight_of(key[i], m);
+      sum += p[i];
+    }
+    sum = wave_sum(sum);
+    const float f = sum > 0.f ? mean / sum : 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) p[i] = -p[i] * f;
+  }
+  for (int j = 0; j < k; ++j) {
+    const int e = (int)lane_of((uint32_t)id, j) - lane * V;
+    const float v = __uint_as_float(lane_of(__float_as_uint(g), j));
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (e == i) p[i] += v;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (lane * V + i < E) {
+      const size_t at = (size_t)t * E + lane * V + i;
+      if (BF) static_cast<uint16_t *>(dlogits)[at] = (uint16_t)bf16_of(p[i]);
+      else static_cast<float *>(dlogits)[at] = p[i];
+    }
+}
+
+int check_topk(const void *logits, const void *ids, const void *w, int T, int E, int k, float scale) {
+  if (T < 0 || E < 1 || k < 1 || k > E || !(scale > 0.f) || !std::isfinite(scale))
+    return FP8GEMM_INVALID_ARG;
+  if (T == 0) return -1;
+  if (!logits || !ids || !w) return FP8GEMM_INVALID_ARG;
+  if (E > 1024 || k > 64 || (long long)T * E >= LIM) return FP8GEMM_UNSUPPORTED_SHAPE;
+  if (!aligned(logits, 16) || !aligned(ids, 4) || !aligned(w, 4)) return FP8GEMM_MISALIGNED;
+  return FP8GEMM_OK;
+}
+
+template <bool BF>
+int topk(const void *logits, int32_t *ids, float *w, int T, int E, int k, int renorm, float scale,
+         void *stream) {
+  const int st = check_topk(logits, ids, w, T, E, k, scale);
+  if (st != FP8GEMM_OK) return st < 0 ? FP8GEMM_OK : st;
+  void *args[] = {&logits, &ids, &w, &T, &E, &k, &renorm, &scale};
+  const void *f = E <= 64    ? reinterpret_cast<const void *>(&topk_kernel<1, BF>)
+                  : E <= 128 ? reinterpret_cast<const void *>(&topk_kernel<2, BF>)
+                  : E <= 256 ? reinterpret_cast<const void *>(&topk_kernel<4, BF>)
+                  : E <= 512 ? reinterpret_cast<const void *>(&topk_kernel<8, BF>)
+                             : reinterpret_cast<const void *>(&topk_kernel<16, BF>);
+  return launch(f, dim3((T + 3) / 4), dim3(256), args, stream);
+}
+
+template <bool BF>
+int topk_backward(const void *logits, const int32_t *ids, const float *w, const float *dw,
+                  void *dlogits, int T, int E, int k, int renorm, float scale, void *stream) {
+  const int st = check_topk(logits, ids, w, T, E, k, scale);
+  if (st != FP8GEMM_OK) return st < 0 ? FP8GEMM_OK : st;
+  if (!dw || !dlogits) return FP8GEMM_INVALID_ARG;
+  if (!aligned(dw, 4) || !aligned(dlogits, 16)) return FP8GEMM_MISALIGNED;
+  void *args[] = {&logits, &ids, &w, &dw, &dlogits, &T, &E, &k, &renorm, &scale};
+  const void *f = E <= 64    ? reinterpret_cast<const void *>(&topk_backward_kernel<1, BF>)
+                  : E <= 128 ? reinterpret_cast<const void *>(&topk_backward_kernel<2, BF>)
+                  : E <= 256 ? reinterpret_cast<const void *>(&topk_backward_kernel<4, BF>)
+                  : E <= 512 ? reinterpret_cast<const void *>(&topk_backward_kernel<8, BF>)
+                             : reinterpret_cast<const void *>(&topk_backward_kernel<16, BF>);
+  return launch(f, dim3((T + 3) / 4), dim3(256), args, stream);
+}
+
+// ---- sorting by expert -----------------------------------------------------
+// A workgroup of 16 waves takes a chunk of 4096 choices, each wave 256 of them
+// in order.  A choice's rank is the number of its expert's choices in earlier
+// chunks, in earlier waves of its chunk (a per-wave count in LDS), in earlier
+// groups of 64 of its wave (the same count, advanced group by group), and on
+// lower lanes of its group (ballots over the expert's bits).  With one chunk
+// a single launch does everything; with more, a first launch writes each
+// chunk's counts, and every workgroup of the second sums what it needs.
+constexpr int CHUNK = 4096, SORT_THREADS = 1024, SORT_WAVES = SORT_THREADS / 64;
+constexpr int PER_WAVE = CHUNK / SORT_WAVES;
+constexpr int MAX_G = 1024;
+
+__global__ __launch_bounds__(SORT_THREADS) void sort_count_kernel(const int32_t *ids, int32_t *ws,
+                                                                  int S, int G) {
+  __shared__ int cnt[MAX_G];
+  const int tid = threadIdx.x;
+  if (tid < G) cnt[tid] = 0;
+  __syncthreads();
+  const long long s0 = (long long)blockIdx.x * CHUNK;
+#pragma unroll
+  for (int i = 0; i < CHUNK / SORT_THREADS; ++i) {
+    const long long s = s0 + i * SORT_THREADS + tid;
+    if (s < S) {
+      const int g = ids[s];
+      if (g >= 0 && g < G) atomicAdd(&cnt[g], 1);
+    }
+  }
+  __syncthreads();
+  if (tid < G) ws[(size_t)blockIdx.x * G + tid] = cnt[tid];
+}
+
+// MASKED: row = g M + rank, counts = min(count, M), no m_indices
+template <bool MASKED>
+__global__ __launch_bounds__(SORT_THREADS) void sort_place_kernel(const int32_t *ids, int32_t *row,
+                                                                  int32_t *m_indices, int32_t *counts,
+                                                                  const int32_t *ws, int S, int G, int M,
+                                                                  int chunks) {
+  __shared__ int cnt[SORT_WAVES][MAX_G];  // counts of each wave, then the rows that its choices take next
+  __shared__ int s_first[MAX_G + 1], s_end[MAX_G];  // an expert's first row, and the first after its last choice
+  __shared__ int s_wave[SORT_WAVES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  for (int i = tid; i < SORT_WAVES * G; i += SORT_THREADS) cnt[i / G][i % G] = 0;
+  __syncthreads();
+  const int s0 = blockIdx.x * CHUNK + wave * PER_WAVE;
+  int id[PER_WAVE / 64];
+#pragma unroll
+  for (int i = 0; i < PER_WAVE / 64; ++i) {
+    const int s = s0 + i * 64 + lane;
+    int g = s < S ? ids[s] : -1;
+    if (g < 0 || g >= G) g = -1;
+    id[i] = g;
+    if (g >= 0) atomicAdd(&cnt[wave][g], 1);
+  }
+  __syncthreads();
+  // expert tid: its choices in earlier chunks and in all
+  int before = 0, total = 0;
+  if (tid < G) {
+    if (chunks > 1) {
+      for (int c = 0; c < chunks; ++c) {
+        const int n = ws[(size_t)c * G + tid];
+        before += c < (int)blockIdx.x ? n : 0;
+        total += n;
+      }
+    } else {
+      for (int v = 0; v < SORT_WAVES; ++v) total += cnt[v][tid];
+    }
+  }
+  int first = tid * M;
+  if (!MASKED) {
+    // exclusive sum over the experts of their counts rounded up to 128
+    const int size = tid < G ? (total + 127) / 128 * 128 : 0;
+    int x = size;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int y = __shfl_up(x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 63) s_wave[wave] = x;
+    __syncthreads();
+    for (int v = 0; v < wave; ++v) x += s_wave[v];
+    first = x - size;
+    if (tid < G) {
+      s_first[tid] = first;
+      s_end[tid] = first + total;
+    }
+    if (tid == G - 1) s_first[G] = x;
+  }
+  if (tid < G) {
+    int next = first + before;
+    for (int v = 0; v < SORT_WAVES; ++v) {
+      const int n = cnt[v][tid];
+      cnt[v][tid] = next;
+      next += n;
+    }
+    if (blockIdx.x == 0) counts[tid] = MASKED ? min(total, M) : total;
+  }
+  __syncthreads();
+  if (!MASKED) {
+    // padding: each expert's, a wave at a time, then the rows past the last expert
+    for (int g = blockIdx.x * SORT_WAVES + wave; g < G; g += gridDim.x * SORT_WAVES)
+      for (int r = s_end[g] + lane; r < s_first[g + 1] && r < M; r += 64) m_indices[r] = -1;
+    for (long long r = (long long)s_first[G] + blockIdx.x * SORT_THREADS + tid; r < M;
+         r += (long long)gridDim.x * SORT_THREADS)
+      m_indices[r] = -1;
+  }
+#pragma unroll
+  for (int i = 0; i < PER_WAVE / 64; ++i) {
+    const int s = s0 + i * 64 + lane;
+    const int g = id[i];
+    // the lanes with this lane's expert
+    unsigned long long same = __ballot(g >= 0);
+    for (int b = 0; (1 << b) < G; ++b) {
+      const unsigned long long set = __ballot((g >> b) & 1);
+      same &= (g >> b) & 1 ? set : ~set;
+    }
+    const int rank = __popcll(same & ((1ull << lane) - 1));
+    int r = -1;
+    if (g >= 0) r = cnt[wave][g] + rank;
+    // every lane has read before the last lane of each expert advances it
+    __builtin_amdgcn_wave_barrier();
+    if (g >= 0 && lane == 63 - __builtin_clzll(same)) cnt[wave][g] = r + 1;
+    __builtin_amdgcn_wave_barrier();
+    if (s < S) {
+      const bool ok = g >= 0 && (MASKED ? r < (g + 1) * M : r < M);
+      row[s] = ok ? r : -1;
+      if (!MASKED && ok) m_indices[r] = g;
+    }
+  }
+}
+
+int sort(const int32_t *ids, int32_t *row, int32_t *m_indices, int32_t *counts, int32_t *ws, int S,
+         int G, int M, bool masked, void *stream) {
+  if (S < 0 || G < 1 || M < 0) return FP8GEMM_INVALID_ARG;
+  if (G > MAX_G) return FP8GEMM_UNSUPPORTED_SHAPE;
+  // every row number that the kernel forms, dropped ones included, fits an int
+  const long long top = (masked ? (long long)G * M : 127LL * G) + S + CHUNK;
+  if (top >= LIM || (!masked && M % 128 != 0)) return FP8GEMM_UNSUPPORTED_SHAPE;
+  if (!counts || (S > 0 && (!ids || !row)) || (!masked && M > 0 && !m_indices) ||
+      (moe_sort_workspace(S, G) > 0 && !ws))
+    return FP8GEMM_INVALID_ARG;
+  if (!aligned(ids, 4) || !aligned(row, 4) || !aligned(m_indices, 4) || !aligned(counts, 4) ||
+      !aligned(ws, 4))
+    return FP8GEMM_MISALIGNED;
+  int chunks = std::max(1, (S + CHUNK - 1) / CHUNK);
+  if (chunks > 1) {
+    void *args[] = {&ids, &ws, &S, &G};
+    const int st = launch(reinterpret_cast<const void *>(&sort_count_kernel), dim3(chunks),
+                          dim3(SORT_THREADS), args, stream);
+    if (st != FP8GEMM_OK) return st;
+  }
+  void *args[] = {&ids, &row, &m_indices, &counts, &ws, &S, &G, &M, &chunks};
+  return launch(masked ? reinterpret_cast<const void *>(&sort_place_kernel<true>)
+                       : reinterpret_cast<const void *>(&sort_place_kernel<false>),
+                dim3(chunks), dim3(SORT_THREADS), args, stream);
+}
+
+// ---- tokens to rows and back -----------------------------------------------
+constexpr int ROW_THREADS = 256;
+
+// The token of a workgroup of a (pieces of a row, T) grid: workgroups go round
+// robin to the 8 XCDs, and each XCD takes a run of consecutive tokens, so
+// neighbouring rows and scales of an expert are written from one L2.
+__device__ __forceinline__ void token_piece(int T, int pieces, int &t, int &piece) {
+  const int n = T * pieces, b = blockIdx.x;
+  const int x = b % 8, per = n / 8, rem = n % 8;
+  const int item = x * per + min(x, rem) + b / 8;
+  t = item / pieces;
+  piece = item % pieces;
+}
+
+// V elements per thread: 8 (16 bytes) where H and the pointers allow, else 1
+template <int V>
+__global__ __launch_bounds__(ROW_THREADS) void dispatch_bf16_kernel(const uint16_t *X, const int32_t *row,
+                                                                    uint16_t *A, int T, int H, int k,
+                                                                    int rows, int pieces) {
+  int t, piece;
+  token_piece(T, pieces, t, piece);
+  const int h = (piece * ROW_THREADS + threadIdx.x) * V;
+  if (h >= H) return;
+  const int32_t *rt = row + (size_t)t * k;
+  if (V == 8) {
+    const u32x4 v = *reinterpret_cast<const u32x4 *>(X + (size_t)t * H + h);
+    for (int j = 0; j < k; ++j) {
+      const int r = rt[j];
+      if (r >= 0 && r < rows) *reinterpret_cast<u32x4 *>(A + (size_t)r * H + h) = v;
+    }
+  } else {
+    const uint16_t v = X[(size_t)t * H + h];
+    for (int j = 0; j < k; ++j) {
+      const int r = rt[j];
+      if (r >= 0 && r < rows) A[(size_t)r * H + h] = v;
+    }
+  }
+}
+
+// 16 elements per thread, 8 threads per 128-wide block: the block is quantised
+// once and its codes and scale go to the token's k rows.
+__global__ __launch_bounds__(ROW_THREADS) void dispatch_fp8_kernel(const uint16_t *X, const int32_t *row,
+                                                                   uint8_t *A, float *sa, int T, int H,
+                                                                   int k, int M, int rows, int pieces) {
+  int t, piece;
+  token_piece(T, pieces, t, piece);
+  const int h = (piece * ROW_THREADS + threadIdx.x) * 16;
+  if (h >= H) return;  // whole 8-thread groups: H is a multiple of 128
+  const u32x4 *src = reinterpret_cast<const u32x4 *>(X + (size_t)t * H + h);
+  const u32x4 v[2] = {src[0], src[1]};
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[2 * i] = bf16_lo(v[i / 4][i % 4]);
+    x[2 * i + 1] = bf16_hi(v[i / 4][i % 4]);
+  }
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) amax = fmaxf(amax, fabsf(x[i]));  // NaN operands are skipped
+  amax = fmaxf(amax, __uint_as_float(dpp<DPP_XOR1>(__float_as_uint(amax))));
+  amax = fmaxf(amax, __uint_as_float(dpp<DPP_XOR2>(__float_as_uint(amax))));
+  amax = fmaxf(amax, __uint_as_float(dpp<DPP_HALF_MIRROR>(__float_as_uint(amax))));
+  const float s = amax == 0.f ? 1.f : amax / 448.f;
+  const E4m3Quotient qd(amax, s);
+  u32x4 c;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    c[i] = e4m3_pack4(qd.quotient(x[4 * i]), qd.quotient(x[4 * i + 1]), qd.quotient(x[4 * i + 2]),
+                      qd.quotient(x[4 * i + 3]), x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+  const int32_t *rt = row + (size_t)t * k;
+  for (int j = 0; j < k; ++j) {
+    const int r = rt[j];
+    if (r < 0 || r >= rows) continue;
+    *reinterpret_cast<u32x4 *>(A + (size_t)r * H + h) = c;
+    if ((threadIdx.x & 7) == 0) sa[((size_t)(r / M) * (H / 128) + h / 128) * M + r % M] = s;
+  }
+}
+
+template <int V>
+__global__ __launch_bounds__(ROW_THREADS) void combine_kernel(const uint16_t *Y, const int32_t *row,
+                                                              const float *w, uint16_t *out, int T,
+                                                              int H, int k, int M, int pieces) {
+  int t, piece;
+  token_piece(T, pieces, t, piece);
+  const int h = (piece * ROW_THREADS + threadIdx.x) * V;
+  if (h >= H) return;
+  const int32_t *rt = row + (size_t)t * k;
+  const float *wt = w + (size_t)t * k;
+  float acc[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+#pragma unroll 4
+  for (int j = 0; j < k; ++j) {
+    const int r = rt[j];
+    if (r < 0 || r >= M) continue;
+    const float f = w ? wt[j] : 1.f;
+    if (V == 8) {
+      const u32x4 y = *reinterpret_cast<const u32x4 *>(Y + (size_t)r * H + h);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[(2 * i) % V] = __builtin_fmaf(f, bf16_lo(y[i]), acc[(2 * i) % V]);
+        acc[(2 * i + 1) % V] = __builtin_fmaf(f, bf16_hi(y[i]), acc[(2 * i + 1) % V]);
+      }
+    } else {
+      acc[0] = __builtin_fmaf(f, __uint_as_float((uint32_t)Y[(size_t)r * H + h] << 16), acc[0]);
+    }
+  }
+  if (V == 8) {
+    u32x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = bf16_pair(acc[(2 * i) % V], acc[(2 * i + 1) % V]);
+    *reinterpret_cast<u32x4 *>(out + (size_t)t * H + h) = o;
+  } else {
+    out[(size_t)t * H + h] = (uint16_t)bf16_of(acc[0]);
+  }
+}
+
+// One workgroup per token.  Eight choices at a time share one reading of dout;
+// their products with Y are summed per thread, then over the wave and, through
+// LDS, over the four waves in order.
+template <int V>
+__global__ __launch_bounds__(ROW_THREADS) void combine_backward_kernel(const uint16_t *dout,
+                                                                       const uint16_t *Y,
+                                                                       const int32_t *row, const float *w,
+                                                                       uint16_t *dY, float *dw, int T,
+                                                                       int H, int k, int M) {
+  constexpr int KB = 8, WAVES = ROW_THREADS / 64;
+  __shared__ float s_dot[WAVES][KB];
+  int t, piece;
+  token_piece(T, 1, t, piece);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int j0 = 0; j0 < k; j0 += KB) {
+    float dot[KB], f[KB];
+    int r[KB];
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+      dot[j] = 0.f;
+      r[j] = -1;
+      f[j] = 0.f;
+      if (j0 + j < k) {
+        r[j] = row[(size_t)t * k + j0 + j];
+        if (r[j] >= M) r[j] = -1;
+        f[j] = w[(size_t)t * k + j0 + j];
+      }
+    }
+    for (int h = threadIdx.x * V; h < H; h += ROW_THREADS * V) {
+      if (V == 8) {
+        const u32x4 d = *reinterpret_cast<const u32x4 *>(dout + (size_t)t * H + h);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          if (r[j] < 0) continue;
+          const u32x4 y = *reinterpret_cast<const u32x4 *>(Y + (size_t)r[j] * H + h);
+          u32x4 o;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            dot[j] = __builtin_fmaf(bf16_lo(d[i]), bf16_lo(y[i]), dot[j]);
+            dot[j] = __builtin_fmaf(bf16_hi(d[i]), bf16_hi(y[i]), dot[j]);
+            o[i] = bf16_pair(f[j] * bf16_lo(d[i]), f[j] * bf16_hi(d[i]));
+          }
+          *reinterpret_cast<u32x4 *>(dY + (size_t)r[j] * H + h) = o;
+        }
+      } else {
+        const float d = __uint_as_float((uint32_t)dout[(size_t)t * H + h] << 16);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          if (r[j] < 0) continue;
+          const size_t at = (size_t)r[j] * H + h;
+          dot[j] = __builtin_fmaf(d, __uint_as_float((uint32_t)Y[at] << 16), dot[j]);
+          dY[at] = (uint16_t)bf16_of(f[j] * d);
+        }
+      }
+    }
+    if (j0 > 0) __syncthreads();  // the group before has been read
+#pragma unroll
+    for (int j = 0; j < KB; ++j) {
+      const float s = wave_sum(dot[j]);
+      if (lane == 0) s_dot[wave][j] = s;
+    }
+    __syncthreads();
+    if ((int)threadIdx.x < KB && j0 + (int)threadIdx.x < k) {
+      float s = 0.f;
+#pragma unroll
+      for (int v = 0; v < WAVES; ++v) s += s_dot[v][threadIdx.x];
+      dw[(size_t)t * k + j0 + threadIdx.x] = s;  // 0 for a choice without a row
+    }
+  }
+}
+
+int check_rows(const void *P, const void *Q, const int32_t *row, int T, int H, int k, int M, int G) {
+  if (T < 0 || H < 0 || k < 1 || M < 0 || G < 1) return FP8GEMM_INVALID_ARG;
+  if (T == 0 || H == 0) return -1;
+  if ((long long)T * k >= LIM || (long long)G * M >= LIM || H > LIM - ROW_THREADS * 16)
+    return FP8GEMM_UNSUPPORTED_SHAPE;
+  if (!P || !Q || !row) return FP8GEMM_INVALID_ARG;
+  if (!aligned(P, 16) || !aligned(Q, 16) || !aligned(row, 4)) return FP8GEMM_MISALIGNED;
+  return FP8GEMM_OK;
+}
+
+// pieces of a row for V elements a thread; false if the grid would be too large
+bool row_pieces(int T, int H, int V, int &pieces, dim3 &grid) {
+  pieces = (int)(((long long)H + (long long)ROW_THREADS * V - 1) / (ROW_THREADS * V));
+  if ((long long)T * pieces >= LIM) return false;
+  grid = dim3((unsigned)(T * pieces));
+  return true;
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_topk_f32(const float *logits, int32_t *ids, float *w, int T, int E, int k, int renorm,
+                 float scale, void *stream) {
+  return topk<false>(logits, ids, w, T, E, k, renorm, scale, stream);
+}
+
+int moe_topk_bf16(const void *logits, int32_t *ids, float *w, int T, int E, int k, int renorm,
+                  float scale, void *stream) {
+  return topk<true>(logits, ids, w, T, E, k, renorm, scale, stream);
+}
+
+int moe_topk_backward_f32(const float *logits, const int32_t *ids, const float *w, const float *dw,
+                          float *dlogits, int T, int E, int k, int renorm, float scale,
+                          void *stream) {
+  return topk_backward<false>(logits, ids, w, dw, dlogits, T, E, k, renorm, scale, stream);
+}
+
+int moe_topk_backward_bf16(const void *logits, const int32_t *ids, const float *w, const float *dw,
+                           void *dlogits, int T, int E, int k, int renorm, float scale,
+                           void *stream) {
+  return topk_backward<true>(logits, ids, w, dw, dlogits, T, E, k, renorm, scale, stream);
+}
+
+int moe_contiguous_rows(int S, int G) {
+  if (S < 0 || G < 1) return 0;
+  const long long rows = ((long long)S + 127LL * std::min(G, S)) / 128 * 128;
+  return rows < LIM ? (int)rows : 0;
+}
+
+int moe_sort_workspace(int S, int G) {
+  if (S <= CHUNK || G < 1 || G > MAX_G) return 0;
+  const long long n = ((long long)S + CHUNK - 1) / CHUNK * G;
+  return n < LIM ? (int)n : 0;
+}
+
+int moe_sort_contiguous(const int32_t *ids, int32_t *row, int32_t *m_indices, int32_t *counts,
+                        int32_t *ws, int S, int G, int M, void *stream) {
+  return sort(ids, row, m_indices, counts, ws, S, G, M, false, stream);
+}
+
+int moe_sort_masked(const int32_t *ids, int32_t *row, int32_t *masked_m, int32_t *ws, int S, int G,
+                    int M, void *stream) {
+  return sort(ids, row, nullptr, masked_m, ws, S, G, M, true, stream);
+}
+
+int moe_dispatch_bf16(const void *X, const int32_t *row, void *A, int T, int H, int k, int M, int G,
+                      void *stream) {
+  const int st = check_rows(X, M == 0 ? X : A, row, T, H, k, M, G);
+  if (st != FP8GEMM_OK) return st < 0 ? FP8GEMM_OK : st;
+  if (M == 0) return FP8GEMM_OK;  // no row to write
+  const bool vec = H % 8 == 0;
+  int rows = M * G, pieces;
+  dim3 grid;
+  if (!row_pieces(T, H, vec ? 8 : 1, pieces, grid)) return FP8GEMM_UNSUPPORTED_SHAPE;
+  void *args[] = {&X, &row, &A, &T, &H, &k, &rows, &pieces};
+  return launch(vec ? reinterpret_cast<const void *>(&dispatch_bf16_kernel<8>)
+                    : reinterpret_cast<const void *>(&dispatch_bf16_kernel<1>),
+                grid, dim3(ROW_THREADS), args, stream);
+}
+
+int moe_dispatch_fp8(const void *X, const int32_t *row, void *A, float *sa, int T, int H, int k,
+                     int M, int G, void *stream) {
+  const int st = check_rows(X, M == 0 ? X : A, row, T, H, k, M, G);
+  if (st != FP8GEMM_OK) return st < 0 ? FP8GEMM_OK : st;
+  if (H % 128 != 0) return FP8GEMM_UNSUPPORTED_SHAPE;
+  if (M == 0) return FP8GEMM_OK;  // no row to write
+  if (!sa) return FP8GEMM_INVALID_ARG;
+  if (!aligned(sa, 4)) return FP8GEMM_MISALIGNED;
+  int rows = M * G, pieces;
+  dim3 grid;
+  if (!row_pieces(T, H, 16, pieces, grid)) return FP8GEMM_UNSUPPORTED_SHAPE;
+  void *args[] = {&X, &row, &A, &sa, &T, &H, &k, &M, &rows, &pieces};
+  return launch(reinterpret_cast<const void *>(&dispatch_fp8_kernel), grid, dim3(ROW_THREADS), args,
+                stream);
+}
+
+int moe_combine_bf16(const void *Y, const int32_t *row, const float *w, void *out, int T, int H,
+                     int k, int M, void *stream) {
+  const int st = check_rows(M == 0 ? out : Y, out, row, T, H, k, M, 1);  // no row: Y is not read
+  if (st != FP8GEMM_OK) return st < 0 ? FP8GEMM_OK : st;
+  if (!aligned(w, 4)) return FP8GEMM_MISALIGNED;
+  const bool vec = H % 8 == 0;
+  int pieces;
+  dim3 grid;
+  if (!row_pieces(T, H, vec ? 8 : 1, pieces, grid)) return FP8GEMM_UNSUPPORTED_SHAPE;
+  void *args[] = {&Y, &row, &w, &out, &T, &H, &k, &M, &pieces};
+  return launch(vec ? reinterpret_cast<const void *>(&combine_kernel<8>)
+                    : reinterpret_cast<const void *>(&combine_kernel<1>),
+                grid, dim3(ROW_THREADS), args, stream);
+}
+
+int moe_combine_backward_bf16(const void *dout, const void *Y, const int32_t *row, const float *w,
+                              void *dY, float *dw, int T, int H, int k, int M, void *stream) {
+  if (T < 0 || H < 0 || k < 1 || M < 0) return FP8GEMM_INVALID_ARG;
+  if (T == 0) return FP8GEMM_OK;
+  if ((long long)T * k >= LIM || H > LIM - ROW_THREADS * 8) return FP8GEMM_UNSUPPORTED_SHAPE;
+  if (!row || !w || !dw || (H > 0 && (!dout || (M > 0 && (!Y || !dY || dY == Y)))))
+    return FP8GEMM_INVALID_ARG;  // H == 0 writes dw alone
+  if (!aligned(dout, 16) || !aligned(Y, 16) || !aligned(dY, 16) || !aligned(row, 4) || !aligned(w, 4) ||
+      !aligned(dw, 4))
+    return FP8GEMM_MISALIGNED;
+  void *args[] = {&dout, &Y, &row, &w, &dY, &dw, &T, &H, &k, &M};
+  return launch(H % 8 == 0 ? reinterpret_cast<const void *>(&combine_backward_kernel<8>)
+                           : reinterpret_cast<const void *>(&combine_backward_kernel<1>),
+                dim3(T), dim3(ROW_THREADS), args, stream);
+}
+
+}  // extern "C"

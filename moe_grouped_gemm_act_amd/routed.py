@@ -1,0 +1,245 @@
+"""Rows routed to one of many weights: the binding of include/fp8gemm_routed.h.
+
+Argument marshalling only, as in the package's other calls; every function
+below is also a name of the package itself.
+
+Example (one MoE layer from tokens to tokens; x bf16 [T,H], logits [T,E])::
+
+    import moe_grouped_gemm_act_amd as fg
+    ids, w = fg.moe_topk(logits, k)
+    row, m_indices, counts = fg.moe_sort_contiguous(ids, E)
+    A, sa = fg.moe_dispatch_fp8(x, row, m_indices.numel())
+    Y, sy = fg.grouped_contiguous_swiglu_fp8(A, sa, W13, s13, m_indices)
+    D = fg.grouped_contiguous(Y, sy, W2, s2, m_indices)
+    out = fg.moe_combine(D, row, w)                    # bf16 [T,H]
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+import os
+
+import torch
+
+from . import HEADER, _check, _codes, _dev, _p, _shape, _stream, load_library
+
+ROUTED_HEADER = os.path.join(os.path.dirname(HEADER), "fp8gemm_routed.h")
+
+__all__ = ["moe_topk", "moe_topk_backward", "moe_contiguous_rows", "moe_sort_contiguous",
+           "moe_sort_masked", "moe_dispatch_bf16", "moe_dispatch_fp8", "moe_dispatch_backward",
+           "moe_combine", "moe_combine_backward"]
+
+_routed = None
+
+
+def _load():
+    global _routed
+    if _routed is None:
+        lib = load_library()
+        vp, i32, f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_float
+        for name, args in (
+                ("moe_topk_f32", [vp, vp, vp, i32, i32, i32, i32, f32, vp]),
+                ("moe_topk_bf16", [vp, vp, vp, i32, i32, i32, i32, f32, vp]),
+                ("moe_topk_backward_f32", [vp] * 5 + [i32, i32, i32, i32, f32, vp]),
+                ("moe_topk_backward_bf16", [vp] * 5 + [i32, i32, i32, i32, f32, vp]),
+                ("moe_contiguous_rows", [i32, i32]),
+                ("moe_sort_workspace", [i32, i32]),
+                ("moe_sort_contiguous", [vp] * 5 + [i32, i32, i32, vp]),
+                ("moe_sort_masked", [vp] * 4 + [i32, i32, i32, vp]),
+                ("moe_dispatch_bf16", [vp] * 3 + [i32] * 5 + [vp]),
+                ("moe_dispatch_fp8", [vp] * 4 + [i32] * 5 + [vp]),
+                ("moe_combine_bf16", [vp] * 4 + [i32] * 4 + [vp]),
+                ("moe_combine_backward_bf16", [vp] * 6 + [i32] * 4 + [vp])):
+            f = getattr(lib, name)
+            f.argtypes, f.restype = args, i32
+        _routed = lib
+    return _routed
+
+
+def _typed(t, dtype, name):
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t
+
+
+def _out(t, shape, dtype, device, name):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _shape(_typed(t, dtype, name), shape, name)
+    return t
+
+
+def moe_topk(logits, k, renormalize=True, scale=1.0, ids=None, w=None, stream=None):
+    """The router's choice: logits [T,E] (float32 or bfloat16) -> (ids [T,k]
+    int32, w [T,k] float32), the k greatest logits in descending order (ties to
+    the lowest index) and scale times their softmax over all experts or, with
+    renormalize, over the chosen ones.  Logits of -inf or NaN are no choice;
+    where fewer than k are left, the id is -1 and the weight 0."""
+    T, E = logits.shape
+    f32 = logits.dtype == torch.float32
+    if not f32:
+        _typed(logits, torch.bfloat16, "logits")
+    ids = _out(ids, (T, k), torch.int32, logits.device, "ids")
+    w = _out(w, (T, k), torch.float32, logits.device, "w")
+    dev = _dev(logits, ids, w)
+    lib = _load()
+    _check((lib.moe_topk_f32 if f32 else lib.moe_topk_bf16)(
+        _p(logits), _p(ids), _p(w), T, E, k, int(renormalize), scale, _stream(stream, dev)))
+    return ids, w
+
+
+def moe_topk_backward(logits, ids, w, dw, renormalize=True, scale=1.0, dlogits=None, stream=None):
+    """dlogits [T,E] (the logits' type) from dw [T,k] float32 and the forward
+    call's logits, ids and w (renormalize and scale as there)."""
+    T, E = logits.shape
+    f32 = logits.dtype == torch.float32
+    if not f32:
+        _typed(logits, torch.bfloat16, "logits")
+    k = ids.shape[1]
+    _shape(_typed(ids, torch.int32, "ids"), (T, k), "ids")
+    _shape(_typed(w, torch.float32, "w"), (T, k), "w")
+    _shape(_typed(dw, torch.float32, "dw"), (T, k), "dw")
+    dlogits = _out(dlogits, (T, E), logits.dtype, logits.device, "dlogits")
+    dev = _dev(logits, ids, w, dw, dlogits)
+    lib = _load()
+    _check((lib.moe_topk_backward_f32 if f32 else lib.moe_topk_backward_bf16)(
+        _p(logits), _p(ids), _p(w), _p(dw), _p(dlogits), T, E, k, int(renormalize), scale,
+        _stream(stream, dev)))
+    return dlogits
+
+
+def moe_contiguous_rows(choices, G):
+    """Rows of the contiguous layout that hold any `choices` ids over G experts."""
+    return _load().moe_contiguous_rows(choices, G)
+
+
+def _workspace(lib, S, G, device, stream):
+    n = lib.moe_sort_workspace(S, G)
+    if n == 0:
+        return None, ctypes.c_void_p(0)
+    ws = torch.empty(n, dtype=torch.int32, device=device)
+    if stream is not None:
+        ws.record_stream(stream)  # freed on return; the caching allocator waits for that stream
+    return ws, _p(ws)
+
+
+def moe_sort_contiguous(ids, G, M=None, row=None, m_indices=None, counts=None, stream=None):
+    """Choices sorted by expert for the contiguous layout: ids [T,k] int32
+    (values outside [0,G) belong to no expert) -> (row [T,k] int32, each
+    choice's row or -1; m_indices [M] int32, each row's expert or -1;
+    counts [G] int32).  M (a multiple of 128) defaults to
+    moe_contiguous_rows(T k, G), which holds any ids."""
+    S = ids.numel()
+    dev = ids.device
+    lib = _load()
+    if M is None:
+        M = lib.moe_contiguous_rows(S, G)
+    row = _out(row, ids.shape, torch.int32, dev, "row")
+    m_indices = _out(m_indices, (M,), torch.int32, dev, "m_indices")
+    counts = _out(counts, (G,), torch.int32, dev, "counts")
+    _dev(_typed(ids, torch.int32, "ids"), row, m_indices, counts)
+    ws, wp = _workspace(lib, S, G, dev, stream)
+    _check(lib.moe_sort_contiguous(_p(ids), _p(row), _p(m_indices), _p(counts), wp, S, G, M,
+                                   _stream(stream, dev)))
+    return row, m_indices, counts
+
+
+def moe_sort_masked(ids, G, M, row=None, masked_m=None, stream=None):
+    """Choices sorted by expert for the masked layout of G experts with M rows
+    each: ids [T,k] int32 -> (row [T,k] int32: g * M + the place among expert
+    g's rows, -1 past its M rows; masked_m [G] int32)."""
+    S = ids.numel()
+    dev = ids.device
+    lib = _load()
+    row = _out(row, ids.shape, torch.int32, dev, "row")
+    masked_m = _out(masked_m, (G,), torch.int32, dev, "masked_m")
+    _dev(_typed(ids, torch.int32, "ids"), row, masked_m)
+    ws, wp = _workspace(lib, S, G, dev, stream)
+    _check(lib.moe_sort_masked(_p(ids), _p(row), _p(masked_m), wp, S, G, M, _stream(stream, dev)))
+    return row, masked_m
+
+
+def _rows(rows):
+    """(leading axes of the operand, M, G) of rows = M or (G, M)."""
+    if isinstance(rows, int):
+        return (rows,), rows, 1
+    G, M = rows
+    return (G, M), M, G
+
+
+def moe_dispatch_bf16(X, row, rows, A=None, stream=None):
+    """Tokens copied to their experts' rows: X [T,H] bfloat16, row [T,k] int32
+    -> A [M,H] (rows = M) or [G,M,H] (rows = (G, M)); rows that no choice names
+    keep their contents (those of an A made here are arbitrary)."""
+    T, H = X.shape
+    lead, M, G = _rows(rows)
+    k = row.shape[1]
+    _shape(_typed(row, torch.int32, "row"), (T, k), "row")
+    A = _out(A, (*lead, H), torch.bfloat16, X.device, "A")
+    dev = _dev(_typed(X, torch.bfloat16, "X"), row, A)
+    _check(_load().moe_dispatch_bf16(_p(X), _p(row), _p(A), T, H, k, M, G, _stream(stream, dev)))
+    return A
+
+
+def moe_dispatch_fp8(X, row, rows, A=None, sa=None, stream=None):
+    """moe_dispatch_bf16 with quantize_fp8_1x128 fused: returns (A codes
+    [M,H] or [G,M,H] as uint8, sa [H/128,M] or [G,H/128,M] float32), the
+    operands of the grouped FP8 products."""
+    T, H = X.shape
+    lead, M, G = _rows(rows)
+    k = row.shape[1]
+    _shape(_typed(row, torch.int32, "row"), (T, k), "row")
+    A = _codes(A, "A") if A is not None else None
+    A = _out(A, (*lead, H), torch.uint8, X.device, "A")
+    sa = _out(sa, (*lead[:-1], H // 128, M), torch.float32, X.device, "sa")
+    dev = _dev(_typed(X, torch.bfloat16, "X"), row, A, sa)
+    _check(_load().moe_dispatch_fp8(_p(X), _p(row), _p(A), _p(sa), T, H, k, M, G,
+                                    _stream(stream, dev)))
+    return A, sa
+
+
+def _flat(t):
+    """(rows, row length) of an operand [M,H] or [G,M,H]."""
+    H = t.shape[-1]
+    return math.prod(t.shape[:-1]), H
+
+
+def moe_combine(Y, row, w=None, out=None, stream=None):
+    """Rows summed back to tokens: Y [M,H] or [G,M,H] bfloat16, row [T,k]
+    int32, w [T,k] float32 (None: weights of 1) -> out [T,H] bfloat16,
+    out[t] = sum_j w[t,j] Y[row[t,j]]; a row outside Y adds nothing."""
+    M, H = _flat(Y)
+    T, k = row.shape
+    _typed(row, torch.int32, "row")
+    out = _out(out, (T, H), torch.bfloat16, Y.device, "out")
+    if w is not None:
+        _shape(_typed(w, torch.float32, "w"), (T, k), "w")
+        dev = _dev(_typed(Y, torch.bfloat16, "Y"), row, w, out)
+    else:
+        dev = _dev(_typed(Y, torch.bfloat16, "Y"), row, out)
+    _check(_load().moe_combine_bf16(_p(Y), _p(row), ctypes.c_void_p(0) if w is None else _p(w),
+                                    _p(out), T, H, k, M, _stream(stream, dev)))
+    return out
+
+
+def moe_dispatch_backward(dA, row, dX=None, stream=None):
+    """The gradient of moe_dispatch_bf16 (and of moe_dispatch_fp8, its
+    quantisation passed straight through): dX[t] = sum_j dA[row[t,j]]."""
+    return moe_combine(dA, row, None, dX, stream)
+
+
+def moe_combine_backward(dout, Y, row, w, dY=None, dw=None, stream=None):
+    """The gradients of moe_combine from dout [T,H] bfloat16: (dY, Y's shape,
+    bfloat16: w[t,j] dout[t] at row[t,j], other rows keep their contents;
+    dw [T,k] float32: <dout[t], Y[row[t,j]]>, 0 where there is no row)."""
+    M, H = _flat(Y)
+    T, k = row.shape
+    _typed(row, torch.int32, "row")
+    _shape(_typed(dout, torch.bfloat16, "dout"), (T, H), "dout")
+    _shape(_typed(w, torch.float32, "w"), (T, k), "w")
+    dY = _out(dY, Y.shape, torch.bfloat16, Y.device, "dY")
+    dw = _out(dw, (T, k), torch.float32, Y.device, "dw")
+    dev = _dev(_typed(Y, torch.bfloat16, "Y"), dout, row, w, dY, dw)
+    _check(_load().moe_combine_backward_bf16(_p(dout), _p(Y), _p(row), _p(w), _p(dY), _p(dw), T, H,
+                                             k, M, _stream(stream, dev)))
+    return dY, dw
