@@ -124,6 +124,35 @@ int moe_combine_bf16(const void *Y, const int32_t *row, const float *w, void *ou
 int moe_combine_backward_bf16(const void *dout, const void *Y, const int32_t *row, const float *w,
                               void *dY, float *dw, int T, int H, int k, int M, void *stream);
 
+/*
+ * A shared projection with a low-rank adapter per row:
+ *   h[m] = scale[a] * X[m] La[a]^T,   D[m] = (base product)[m] + h[m] Lb[a]^T,   a = ids[m],
+ * with ids [M] (int32; a value outside [0,G): no adapter, the base product
+ * alone), La [G][R,K] and Lb [G][N,R] (bf16; adapters of smaller rank are
+ * padded with zeros), scale [G] (fp32).  Rows may come in any order; adapters
+ * that no row names are not read.
+ *
+ * lora_shrink_bf16 writes H [M,R] (bf16) = h from X [M,K] (bf16): fp32 sums,
+ * scaled, then one rounding to bf16, the operand type of the second factor's
+ * product.  Rows without an adapter keep H's previous contents.  One H serves
+ * one projection.  The products then add h Lb^T into the base product's fp32
+ * accumulators: D is rounded once.  H of rows without an adapter is not used.
+ * Constraints: K % 64 == 0 (FP8 base: K % 128 == 0 and K <= 20480);
+ * R % 8 == 0, R <= 4096, G <= 4096; M R, N R and G N R below 2^30 (La may be larger);
+ * the base calls' own; X, La, H and Lb 16-byte aligned, ids and scale 4-byte.
+ * M, N, R or G of 0 is allowed (the shrink then does nothing, the products are
+ * the base call); K == 0 gives zeros.
+ */
+int lora_shrink_bf16(const void *X, const void *La, const int32_t *ids, const float *scale, void *H,
+                     int M, int K, int R, int G, void *stream);
+
+int gemm_bf16_nt_lora(const void *A, const void *B, const void *H, const void *Lb, const int32_t *ids,
+                      void *D, int M, int N, int K, int R, int G, void *stream);
+
+int gemm_fp8_1x128_128x128_bf16_lora(const void *A, const float *sa, const void *B, const float *sb,
+                                     const void *H, const void *Lb, const int32_t *ids, void *D, int M,
+                                     int N, int K, int R, int G, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

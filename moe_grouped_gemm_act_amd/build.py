@@ -4,7 +4,7 @@ import subprocess
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
-SRCS = [os.path.join(HERE, "csrc", f) for f in ("fp8gemm.hip", "quant.hip", "moe.hip")]
+SRCS = [os.path.join(HERE, "csrc", f) for f in ("fp8gemm.hip", "quant.hip", "moe.hip", "lora.hip")]
 LIB = os.path.join(HERE, "libfp8gemm.so")
 
 FLAGS = [

@@ -57,6 +57,7 @@
 
 #include "e4m3.h"
 #include "fp8gemm.h"
+#include "fp8gemm_routed.h"
 
 namespace {
 
@@ -87,6 +88,11 @@ struct Args {
   // tail_splits items of tail_kb blocks each, whose fp32 partials go to ws
   // tile by tile and are summed by tail_reduce_kernel
   int full_tiles, tail_splits, tail_kb;
+  // low-rank adapters (dense): rows' ranks h [M][lr] and the adapters' second
+  // factors [lg][N][lr] (both bf16), and each row's adapter
+  const uint16_t *lh, *lb;
+  const int32_t *lids;
+  int lr, lg;
 };
 
 // XOR key of an LDS row: 16-byte chunk c of row r sits at position
@@ -577,8 +583,114 @@ __device__ __forceinline__ void store_bf16(const v4f (&acc)[TN][TM], uint16_t *D
   }
 }
 
+// ---- low-rank adapters in the tile kernel ----------------------------------
+// Row m of a dense product adds h[m] Lb_a^T for its adapter a = ids[m], with
+// h[m] (lr values) formed before (lora_shrink_bf16).  A tile takes that sum as
+// more K blocks behind the base product's, into the same accumulators, so D is
+// rounded once and never read: with a_0 < a_1 < ... the adapters that the
+// tile's rows name, the added K axis is the ranks of a_0, then those of a_1,
+// ..., 64 to a block.  The activation operand there is h where the row's
+// adapter owns the rank and zeros elsewhere, the weight operand
+// Lb[a_i][n][rank]; both come through the loaders' direct-to-LDS loads, 16
+// bytes (8 ranks, always of one adapter) a lane, and a chunk that is not there
+// is an out-of-range load: zeros, no traffic.  So every adapter's rows are read
+// once a weight tile whatever the order of the requests, and a tile pays
+// ceil(adapters lr / 64) blocks beside its K / 64 (BF16) or K / 128 (FP8).
+constexpr int LORA_MAXG = 4096;
+
+// One wave lists the distinct adapters of the tile's BM rows in ascending
+// order (a bitmap over all lg) while the loaders fetch the first blocks.
+template <int BM>
+__device__ __forceinline__ void adapter_list(const Args &a, int m0, int lane, int *s_id, int *s_list,
+                                             uint32_t *s_bits, int *s_n) {
+  s_bits[lane] = 0;
+  s_bits[lane + 64] = 0;
+#pragma unroll
+  for (int i = 0; i < BM / 64; ++i) {
+    const int r = i * 64 + lane;
+    int id = m0 + r < a.M ? a.lids[m0 + r] : -1;
+    if (id < 0 || id >= a.lg) id = -1;
+    s_id[r] = id;
+    if (id >= 0) atomicOr(&s_bits[id >> 5], 1u << (id & 31));
+  }
+  uint32_t w[2] = {s_bits[2 * lane], s_bits[2 * lane + 1]};
+  const int c = __popc(w[0]) + __popc(w[1]);
+  int x = c;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int y = __shfl_up(x, d, 64);
+    if (lane >= d) x += y;
+  }
+  if (lane == 63) *s_n = x;
+  int pos = x - c;
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+    for (; w[h]; w[h] &= w[h] - 1) s_list[pos++] = 64 * lane + 32 * h + __builtin_ctz(w[h]);
+}
+
+// An adapter block of a compute wave: ranks e0 .. e0 + 63 of the added K axis.
+// A row's zeros beside an infinite or NaN weight of another row's adapter would
+// make NaN, so a block whose weights hold one is done without the MFMA, each
+// output from the ranks of its own row's adapter alone.
+template <int TN, int TM, int BM>
+__device__ __forceinline__ void adapter_kblock(const uint8_t *sl, int e0, int R, int n_list, const int *s_id,
+                                               const int *s_list, int wn, int wm, int fr, int fg,
+                                               v4f (&acc)[TN][TM]) {
+  const int lo = fr * BK + chunk_pos(fg, fr), hi = fr * BK + chunk_pos(fg + 4, fr);
+  const uint8_t *pa = sl + wm * TM * 16 * BK, *pb = sl + (BM + wn * TN * 16) * BK;
+  constexpr int G = 16 * BK;  // bytes per 16-row group
+  unsigned wild = 0;  // a bf16 exponent of all ones in the low or high half of any word
+  {
+    v8i bfr[TN];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      bfr[i] = frag_at(pb + i * G + lo, pb + i * G + hi);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) wild |= (((bfr[i][e] & 0x7F807F80u) >> 7) + 0x00010001u) & 0x01000100u;
+    }
+    if (__ballot(wild != 0) == 0) {
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        asm volatile("" ::: "memory");  // one activation fragment at a time
+        const v8i afr = frag_at(pa + j * G + lo, pa + j * G + hi);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < TN; ++i)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf_half(bfr[i], h), bf_half(afr, h),
+                                                                acc[i][j], 0, 0, 0);
+      }
+      return;
+    }
+  }
+  // each output from the ranks of its own row's adapter alone, read from the
+  // slot (rolled loops: the accumulators leave few registers)
+#pragma unroll
+  for (int j = 0; j < TM; ++j) {
+    const int row = (wm * TM + j) * 16 + fr, id = s_id[row];
+#pragma unroll
+    for (int i = 0; i < TN; ++i) {
+      const int wr = BM + (wn * TN + i) * 16 + 4 * fg;
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        const int li = (e0 + 8 * c) / R;
+        if (li >= n_list || s_list[li] != id) continue;
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(sl + row * BK + chunk_pos(c, row));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint16_t *w = reinterpret_cast<const uint16_t *>(sl + (wr + r) * BK + chunk_pos(c, wr + r));
+#pragma unroll 1
+          for (int e = 0; e < 8; ++e)
+            acc[i][j][r] = __builtin_fmaf(__uint_as_float((uint32_t)h[e] << 16),
+                                          __uint_as_float((uint32_t)w[e] << 16), acc[i][j][r]);
+        }
+      }
+    }
+  }
+}
+
 template <int WGN, int WGM, int TN, int TM, int STAGES, int NLD, bool KSPLIT, bool ACT, int LAYOUT,
-          bool BF = false>
+          bool BF = false, bool LORA = false>
 __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
   constexpr int BN = WGN * TN * 16, BM = WGM * TM * 16;
   constexpr int ROWS = BM + BN;
@@ -604,10 +716,14 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
   // 128 columns of y
   static_assert(!ACT || (BN == 256 && WGN == 4 && TN == 4 && BM <= 128), "SwiGLU tile shape");
   static_assert(!(ACT && BF), "the fused SwiGLU takes FP8 operands");
+  static_assert(!LORA || (LAYOUT == DENSE && !ACT && NLD % 2 == 0), "adapters: dense tiles");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES][SLOT];
   __shared__ float s_sb[BN > 128 || TWOB ? 2 : 1][BF ? 1 : MAXKB];
   __shared__ float s_rmax[ACT ? 4 * BM : 1];  // ACT: row maxima of y per wave column
   __shared__ int s_group;
+  // LORA: the rows' adapters, the distinct ones, their bitmap and number
+  __shared__ int s_lid[LORA ? BM : 1], s_llist[LORA ? BM : 1], s_ln;
+  __shared__ uint32_t s_lbits[LORA ? LORA_MAXG / 32 : 1];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -648,6 +764,16 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
   const int m0 = tm * BM, n0 = tn * BN;
   const int kbps = tail ? a.tail_kb : a.kb_per_split;
   const int kb0 = split * kbps, nk = max(0, min(Kb - kb0, kbps));
+  // LORA: this item's share of the tile's adapter blocks (its K split's part):
+  // the first and how many; valid once the list is (one barrier later)
+  auto adapter_blocks = [&](int &first) {
+    const int n = (s_ln * a.lr + 63) / 64, parts = tail ? a.tail_splits : S;
+    first = n * split / parts;
+    return n * (split + 1) / parts - first;
+  };
+  // the loaders' first loads are all of the base product: they need not wait
+  // for the list, which the first block's barrier then publishes
+  const bool list_first = LORA && nk < STAGES - 1;
 
   const uint8_t *A = a.A, *B = a.B;
   const float *sa = a.sa, *sb = a.sb;
@@ -715,12 +841,46 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
       soff[jj] = m0 + j * 64 + lane < mvalid ? (uint32_t)(m0 + j * 64 + lane) * 4 : OOB;
       sdst[jj] = ROWS * BK + j * 256;
     }
+    int nt = nk;  // blocks of this item: the base product's, then (LORA) the adapters'
+    int lb0 = 0;  // LORA: the item's first adapter block
+    const __amdgpu_buffer_rsrc_t rlh = LORA ? rsrc(a.lh, (uint32_t)M * a.lr * 2) : ra;
+    const __amdgpu_buffer_rsrc_t rlb = LORA ? rsrc(a.lb, (uint32_t)a.lg * N * a.lr * 2) : rb;
+    // adapter block t >= nk (blocks past nt load nothing); as many loads as a base block
+    auto adapter_block = [&](int t, uint8_t *sl) {
+      const int col = (lane & 7) ^ row_key(L * 8 + (lane >> 3));  // the same for every q: NLD is even
+      const int e = (lb0 + t - nk) * 64 + col * 8, li = e / a.lr, rank = e - li * a.lr;
+      const bool live = t < nt && li < s_ln;
+      const int ad = live ? s_llist[live ? li : 0] : -2;
+#pragma unroll
+      for (int q = 0; q < DMA; ++q) {
+        const int r = (L + NLD * q) * 8 + (lane >> 3);
+        uint32_t o = OOB;
+        if (q < QA) {
+          if (s_lid[LORA ? r : 0] == ad) o = ((uint32_t)(m0 + r) * a.lr + rank) * 2;
+        } else {
+          const int grow = n0 + r - BM;
+          if (live && grow < N) o = (((uint32_t)ad * N + grow) * a.lr + rank) * 2;
+        }
+        dma16(q < QA ? rlh : rlb, o, sl + (L + NLD * q) * 1024);
+      }
+#pragma unroll
+      for (int jj = 0; jj < SPL; ++jj) dma4(rs, OOB, sl + sdst[jj]);
+    };
+    if (LORA && list_first) {
+      __builtin_amdgcn_s_barrier();  // the list
+      asm volatile("" ::: "memory");
+      nt = nk + adapter_blocks(lb0);
+    }
     // G(t): K block kb0 + t (clamped: blocks past the range re-read the last
     // one and are never consumed) -> slot t % STAGES
 #define TK_G(t)                                                                               \
   do {                                                                                        \
     const int kb_ = kb0 + min((t), nk - 1);                                                   \
     uint8_t *sl_ = lds[(t) % STAGES];                                                         \
+    if (LORA && (t) >= nk) {                                                                  \
+      adapter_block((t), sl_);                                                                \
+      break;                                                                                  \
+    }                                                                                         \
     _Pragma("unroll") for (int q = 0; q < DMA; ++q)                                          \
         dma16(q < QA ? ra : rb, off[q] + (uint32_t)kb_ * BK, sl_ + (L + NLD * q) * 1024);     \
     _Pragma("unroll") for (int jj = 0; jj < SPL; ++jj)                                        \
@@ -730,15 +890,16 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
 #pragma unroll
       for (int t = 0; t < STAGES - 1; ++t) TK_G(t);
     }
-    for (int t0 = 0; t0 < nk; t0 += STAGES) {
+    for (int t0 = 0; t0 < nt; t0 += STAGES) {
 #pragma unroll
       for (int u = 0; u < STAGES; ++u) {
         const int t = t0 + u;
-        if (t >= nk) break;
+        if (t >= nt) break;
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(PER_G * (STAGES - 2)));  // my loads of block t landed
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();  // ... and everyone's; all compute waves are past block t - 1
         asm volatile("" ::: "memory");
+        if (LORA && t == 0 && !list_first) nt = nk + adapter_blocks(lb0);
         TK_G(t + STAGES - 1);
       }
     }
@@ -750,6 +911,15 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
 
   // ---------------- compute waves ----------------
   const int wn = wave % WGN, wm = wave / WGN;
+  if (LORA) {
+    if (wave == 0) adapter_list<LORA ? BM : 64>(a, m0, lane, s_lid, s_llist, s_lbits, &s_ln);
+    __builtin_amdgcn_s_waitcnt(0);  // written before the barrier that publishes it
+    if (list_first) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+    }
+  }
   // which weight-scale block this wave's rows use (ACT: gate block 0, up block 1)
   const int hsb = ACT ? 0 : (wn * TN * 16) / 128;
   // TWOB: the fragments whose rows use the second block (ACT: the up
@@ -814,6 +984,18 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
       }
     }
     fp8_flush<TN, TM, TWOB>(acc, ring, sc_last, himask);
+  }
+  if constexpr (LORA) {
+    int first;
+    const int n = adapter_blocks(first);
+    int slot = nk % STAGES;
+    for (int t = 0; t < n; ++t) {
+      asm volatile("" ::: "memory");
+      __builtin_amdgcn_s_barrier();  // adapter block t is in slot `slot`
+      asm volatile("" ::: "memory");
+      adapter_kblock<TN, TM, BM>(lds[slot], (first + t) * 64, a.lr, s_ln, s_lid, s_llist, wn, wm, fr, fg, acc);
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
+    }
   }
 
   if constexpr (ACT) {
@@ -1507,7 +1689,7 @@ float *scratch_ptr() {
 }
 
 template <int WGN, int WGM, int TN, int TM, int STAGES, int NLD, int LAYOUT, bool KSPLIT = false,
-          bool ACT = false, bool BF = false>
+          bool ACT = false, bool BF = false, bool LORA = false>
 int launch_tile(Args a, int groups, hipStream_t stream) {
   a.tiles_m = cdiv(a.M, WGM * TM * 16);
   a.tiles_n = cdiv(a.N, WGN * TN * 16);
@@ -1518,7 +1700,7 @@ int launch_tile(Args a, int groups, hipStream_t stream) {
   void *kargs[] = {&a};
   hipError_t e = hipLaunchKernel(
       reinterpret_cast<const void *>(
-          &tile_kernel<WGN, WGM, TN, TM, STAGES, NLD, KSPLIT, ACT, LAYOUT, BF>),
+          &tile_kernel<WGN, WGM, TN, TM, STAGES, NLD, KSPLIT, ACT, LAYOUT, BF, LORA>),
       dim3(a.tiles_m * a.tiles_n * a.splits, groups), dim3((WGN * WGM + NLD) * 64), kargs, 0,
       stream);
   return e == hipSuccess ? FP8GEMM_OK : FP8GEMM_LAUNCH_FAILED;
@@ -1586,7 +1768,8 @@ DecodeCfg decode_config(int M, int N, int Kb, bool bf) {
 // BF: bf16 operands, K blocks of 64 elements (128 bytes)
 // fixed_ws: a caller-provided scratch of SCRATCH_FLOATS (the allocation-free
 // entry point); nullptr: the library workspace (WsLease)
-template <bool BF>
+// LORA: with the adapters' blocks (spread over the K splits)
+template <bool BF, bool LORA = false>
 int run_decode(Args a, hipStream_t stream, float *fixed_ws = nullptr) {
   const int Kb = (BF ? 2 * a.K : a.K) / BK;
   DecodeCfg c = decode_config(a.M, a.N, Kb, BF);
@@ -1612,15 +1795,15 @@ int run_decode(Args a, hipStream_t stream, float *fixed_ws = nullptr) {
   int st = FP8GEMM_LAUNCH_FAILED;  // unreachable: decode_config returns built instances only
   if (c.waves == 8) {
     if (c.bn == 128)
-      st = bm == 64 ? launch_tile<2, 4, 4, 1, 4, 4, DENSE, true, false, BF>(a, 1, stream)
-                    : launch_tile<2, 4, 4, 2, 4, 4, DENSE, true, false, BF>(a, 1, stream);
+      st = bm == 64 ? launch_tile<2, 4, 4, 1, 4, 4, DENSE, true, false, BF, LORA>(a, 1, stream)
+                    : launch_tile<2, 4, 4, 2, 4, 4, DENSE, true, false, BF, LORA>(a, 1, stream);
     else
-      st = launch_tile<2, 4, 2, 2, 4, 4, DENSE, true, false, BF>(a, 1, stream);
+      st = launch_tile<2, 4, 2, 2, 4, 4, DENSE, true, false, BF, LORA>(a, 1, stream);
   }
 #define DEC(BN_, ST_)                                                                     \
   if (c.waves == 4 && c.bn == BN_ && c.stages == ST_)                                     \
-    st = bm == 64 ? launch_tile<1, 4, BN_ / 16, 1, ST_, 4, DENSE, true, false, BF>(a, 1, stream) \
-                  : launch_tile<1, 4, BN_ / 16, 2, ST_, 4, DENSE, true, false, BF>(a, 1, stream);
+    st = bm == 64 ? launch_tile<1, 4, BN_ / 16, 1, ST_, 4, DENSE, true, false, BF, LORA>(a, 1, stream) \
+                  : launch_tile<1, 4, BN_ / 16, 2, ST_, 4, DENSE, true, false, BF, LORA>(a, 1, stream);
   DEC(64, 4)
   DEC(64, 6)
   DEC(128, 4)
@@ -1702,7 +1885,8 @@ hipError_t launch_walk(Args &a, int P, hipStream_t stream) {
 // S = min(8, 256 / R) parts (each at least 4 K blocks) that run as the last
 // items of the same grid, and tail_reduce_kernel adds the parts.  Without a
 // workspace the tail is not split.
-template <int WGN, int WGM, int TN, int TM, int STAGES, int NLD, bool BF = false>
+// LORA: one workgroup per tile (the walk has no adapter blocks).
+template <int WGN, int WGM, int TN, int TM, int STAGES, int NLD, bool BF = false, bool LORA = false>
 int launch_dense_large(Args a, hipStream_t stream, float *fixed_ws = nullptr) {
   constexpr int BN = WGN * TN * 16, BM = WGM * TM * 16;
   const int tiles_m = cdiv(a.M, BM), tiles_n = cdiv(a.N, BN), T = tiles_m * tiles_n;
@@ -1720,13 +1904,13 @@ int launch_dense_large(Args a, hipStream_t stream, float *fixed_ws = nullptr) {
   }
   // more tiles than CUs: the persistent walk over the same items
   const int P = walk_workgroups();
-  const bool walk = walk_enabled(BF ? 2 * a.K : a.K) && P >= 8 && T > P;
+  const bool walk = !LORA && walk_enabled(BF ? 2 * a.K : a.K) && P >= 8 && T > P;
   a.tiles_m = tiles_m;
   a.tiles_n = tiles_n;
   a.splits = 1;
   a.kb_per_split = Kb;
   if (S <= 1) {
-    if (!walk) return launch_tile<WGN, WGM, TN, TM, STAGES, NLD, DENSE, false, false, BF>(a, 1, stream);
+    if (!walk) return launch_tile<WGN, WGM, TN, TM, STAGES, NLD, DENSE, false, false, BF, LORA>(a, 1, stream);
     return launch_walk<WGN, WGM, TN, TM, STAGES, NLD, DENSE, BF>(a, P, stream) == hipSuccess
                ? FP8GEMM_OK
                : FP8GEMM_LAUNCH_FAILED;
@@ -1743,7 +1927,7 @@ int launch_dense_large(Args a, hipStream_t stream, float *fixed_ws = nullptr) {
     void *kargs[] = {&a};
     er = hipLaunchKernel(
         reinterpret_cast<const void *>(
-            &tile_kernel<WGN, WGM, TN, TM, STAGES, NLD, false, false, DENSE, BF>),
+            &tile_kernel<WGN, WGM, TN, TM, STAGES, NLD, false, false, DENSE, BF, LORA>),
         dim3(a.full_tiles + R * a.tail_splits), dim3((WGN * WGM + NLD) * 64), kargs, 0, stream);
   }
   if (er != hipSuccess) return FP8GEMM_LAUNCH_FAILED;
@@ -2014,6 +2198,63 @@ int grouped_masked_bf16(const void *A, const void *B, void *D, int M, int N, int
   if (expected_m <= 64)
     return launch_tile<1, 4, 8, 1, 4, 4, MASKED, false, false, true>(a, G, s);
   return launch_tile<1, 4, 8, 2, 4, 4, MASKED, false, false, true>(a, G, s);
+}
+
+// A product with adapters: the arguments beyond the base product's.  Returns
+// -1 where the base call alone is the answer.
+static int check_lora(const void *H, const void *Lb, const int32_t *ids, int M, int N, int K, int R,
+                      int G) {
+  if (R < 0 || G < 0) return FP8GEMM_INVALID_ARG;
+  if (M <= 0 || N <= 0 || K <= 0 || R == 0 || G == 0) return -1;
+  if (!H || !Lb || !ids) return FP8GEMM_INVALID_ARG;
+  if (R % 8 != 0 || G > LORA_MAXG || R > 4096) return FP8GEMM_UNSUPPORTED_SHAPE;
+  const long long lim = 1LL << 30;  // 2^31 bytes
+  if ((long long)M * R >= lim || (long long)N * R >= lim || (long long)G * N * R >= lim)
+    return FP8GEMM_UNSUPPORTED_SHAPE;
+  if (!aligned(H, 16) || !aligned(Lb, 16) || !aligned(ids, 4)) return FP8GEMM_MISALIGNED;
+  return FP8GEMM_OK;
+}
+
+int gemm_bf16_nt_lora(const void *A, const void *B, const void *H, const void *Lb, const int32_t *ids,
+                      void *D, int M, int N, int K, int R, int G, void *stream) {
+  const int sl = check_lora(H, Lb, ids, M, N, K, R, G);
+  if (sl < 0) return gemm_bf16_nt(A, B, D, M, N, K, stream);
+  if (sl != FP8GEMM_OK) return sl;
+  const int st = check_bf16(A, B, D, M, N, K, (long long)M * K, (long long)N * K,
+                            (long long)M * N);
+  if (st != FP8GEMM_OK) return st;
+  Args a{static_cast<const uint8_t *>(A), nullptr, static_cast<const uint8_t *>(B), nullptr,
+         static_cast<uint16_t *>(D), M, N, K, 1, nullptr, 0, 0, 1, 2 * K / BK, nullptr};
+  a.lh = static_cast<const uint16_t *>(H);
+  a.lb = static_cast<const uint16_t *>(Lb);
+  a.lids = ids;
+  a.lr = R;
+  a.lg = G;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (M <= 128) return run_decode<true, true>(a, s);
+  return launch_dense_large<2, 4, 4, 4, 3, 4, true, true>(a, s);
+}
+
+int gemm_fp8_1x128_128x128_bf16_lora(const void *A, const float *sa, const void *B, const float *sb,
+                                     const void *H, const void *Lb, const int32_t *ids, void *D, int M,
+                                     int N, int K, int R, int G, void *stream) {
+  const int sl = check_lora(H, Lb, ids, M, N, K, R, G);
+  if (sl < 0) return gemm_fp8_1x128_128x128_bf16(A, sa, B, sb, D, M, N, K, stream);
+  if (sl != FP8GEMM_OK) return sl;
+  const int st = check_common(A, sa, B, sb, D, M, N, K, (long long)M * K, (long long)N * K,
+                              (long long)M * N);
+  if (st != FP8GEMM_OK) return st;
+  if (K > 20480) return FP8GEMM_UNSUPPORTED_SHAPE;  // past the tile kernel's range
+  Args a{static_cast<const uint8_t *>(A), sa, static_cast<const uint8_t *>(B), sb,
+         static_cast<uint16_t *>(D), M, N, K, 1, nullptr, 0, 0, 1, K / BK, nullptr};
+  a.lh = static_cast<const uint16_t *>(H);
+  a.lb = static_cast<const uint16_t *>(Lb);
+  a.lids = ids;
+  a.lr = R;
+  a.lg = G;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  if (M <= 128) return run_decode<false, true>(a, s);
+  return launch_dense_large<4, 2, 4, 4, 3, 4, false, true>(a, s);
 }
 
 const char *fp8gemm_status_string(int status) {

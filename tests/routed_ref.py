@@ -110,3 +110,16 @@ def combine_backward(dout, Y, row, w, dY):
                 dw[t, j] = np.dot(dout[t], Y[r])
                 mag[t, j] = np.dot(np.abs(dout[t]), np.abs(Y[r]))
     return dY, dw, mag
+
+
+def lora(base, X, La, Lb, ids, scale):
+    """(D, sum of |h||Lb| terms, h) in float64: base [M,N] plus each row's
+    adapter; an id outside [0,G) adds nothing."""
+    D, mag = base.copy(), np.zeros_like(base)
+    h = np.zeros((X.shape[0], La.shape[1]))
+    for m, a in enumerate(ids):
+        if 0 <= a < La.shape[0]:
+            h[m] = float(scale[a]) * (La[a] @ X[m])
+            D[m] = D[m] + Lb[a] @ h[m]
+            mag[m] = np.abs(Lb[a]) @ np.abs(h[m])
+    return D, mag, h

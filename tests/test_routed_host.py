@@ -190,6 +190,43 @@ def test_combine_validation(lib):
     assert bwd(NUL, NUL, NUL, NUL, NUL, NUL, T=0) == OK
 
 
+def test_lora_validation(lib):
+    def shrink(X=P, La=P, ids=P, scale=P, H=Q, M=4, K=128, R=16, G=2):
+        return lib.lora_shrink_bf16(X, La, ids, scale, H, M, K, R, G, NUL)
+
+    def bf16(A=P, B=P, H=P, Lb=P, ids=P, D=Q, M=4, N=64, K=128, R=16, G=2):
+        return lib.gemm_bf16_nt_lora(A, B, H, Lb, ids, D, M, N, K, R, G, NUL)
+
+    def fp8(A=P, sa=P, B=P, sb=P, H=P, Lb=P, ids=P, D=Q, M=4, N=64, K=128, R=16, G=2):
+        return lib.gemm_fp8_1x128_128x128_bf16_lora(A, sa, B, sb, H, Lb, ids, D, M, N, K, R, G, NUL)
+    for call in (shrink, bf16, fp8):
+        assert call(M=-1) == call(K=-128) == call(R=-8) == call(G=-1) == INVALID
+        assert call(H=NUL) == call(ids=NUL) == INVALID
+        assert call(K=100) == call(R=12) == call(R=4104) == call(G=4097) == SHAPE
+        assert call(M=1 << 27, R=16) == SHAPE
+        assert call(H=P_ODD) == call(ids=P_BAD) == MISALIGNED
+    assert shrink(X=NUL) == shrink(La=NUL) == shrink(scale=NUL) == INVALID
+    assert shrink(X=P_ODD) == shrink(La=P_ODD) == shrink(scale=P_BAD) == MISALIGNED
+    assert shrink(NUL, NUL, NUL, NUL, NUL, M=0) == shrink(NUL, NUL, NUL, NUL, NUL, R=0) == OK
+    for call in (bf16, fp8):
+        assert call(N=-1) == call(Lb=NUL) == call(A=NUL) == call(B=NUL) == call(D=NUL) == INVALID
+        assert call(N=1 << 20, G=4096) == SHAPE
+        assert call(Lb=P_ODD) == call(A=P_ODD) == call(D=P_ODD) == MISALIGNED
+        assert call(M=0, A=NUL, B=NUL, H=NUL, Lb=NUL, ids=NUL, D=NUL) == OK
+        assert call(R=0, H=NUL, Lb=NUL, A=NUL) == INVALID  # the base call's own check
+    assert fp8(sa=NUL) == INVALID
+    assert fp8(K=20608) == SHAPE
+
+
+def test_lora_reference_is_the_dense_sum():
+    rng = np.random.default_rng(4200)
+    base, X, La, Lb = rng.normal(size=(3, 4)), rng.normal(size=(3, 6)), rng.normal(size=(2, 5, 6)), rng.normal(size=(2, 4, 5))
+    D, _, h = ref.lora(base, X, La, Lb, [1, -1, 0], [0.5, 2.0])
+    assert np.allclose(D[0], base[0] + 2.0 * X[0] @ (Lb[1] @ La[1]).T)
+    assert (D[1] == base[1]).all() and (h[1] == 0).all()
+    assert np.allclose(D[2], base[2] + 0.5 * X[2] @ (Lb[0] @ La[0]).T)
+
+
 def test_binding_refusals():
     x = torch.zeros((4, 128), dtype=torch.bfloat16)
     row = torch.zeros((4, 2), dtype=torch.int32)
@@ -211,3 +248,10 @@ def test_binding_refusals():
         fg.moe_combine(x, row, w=torch.zeros((4, 3)))
     with pytest.raises(ValueError):
         fg.moe_combine_backward(x[:3], x, row, torch.zeros((4, 2)))
+    La, Lb = torch.zeros((2, 8, 128), dtype=torch.bfloat16), torch.zeros((2, 16, 8), dtype=torch.bfloat16)
+    W, ids, scale = torch.zeros((16, 128), dtype=torch.bfloat16), torch.zeros(4, dtype=torch.int32), torch.ones(2)
+    for bad in ((x, W, La, Lb, ids, scale), (x, W, La, Lb[:1], ids, scale), (x, W, La, Lb, ids[:3], scale)):
+        with pytest.raises(ValueError):
+            fg.gemm_bf16_nt_lora(*bad)
+    with pytest.raises(TypeError):
+        fg.lora_shrink_bf16(x, La.float(), ids, scale)
