@@ -132,26 +132,28 @@ int moe_combine_backward_bf16(const void *dout, const void *Y, const int32_t *ro
  * padded with zeros), scale [G] (fp32).  Rows may come in any order; adapters
  * that no row names are not read.
  *
- * lora_shrink_bf16 writes H [M,R] (bf16) = h from X [M,K] (bf16): fp32 sums,
- * scaled, then one rounding to bf16, the operand type of the second factor's
- * product.  Rows without an adapter keep H's previous contents.  One H serves
- * one projection.  The products then add h Lb^T into the base product's fp32
- * accumulators: D is rounded once.  H of rows without an adapter is not used.
- * Constraints: K % 64 == 0 (FP8 base: K % 128 == 0 and K <= 20480);
- * R % 8 == 0, R <= 4096, G <= 4096; M R, N R and G N R below 2^30 (La may be larger);
- * the base calls' own; X, La, H and Lb 16-byte aligned, ids and scale 4-byte.
- * M, N, R or G of 0 is allowed (the shrink then does nothing, the products are
- * the base call); K == 0 gives zeros.
+ * h is an fp32 sum, scaled and rounded once to bf16 (it is an operand of the
+ * second factor's product); h Lb^T is added into the base product's fp32
+ * accumulators, and D is rounded once.  A value that is not finite in one row
+ * of X or in one adapter reaches the rows that use it alone.
+ * ws: lora_workspace(M, K, R) bytes of the caller's, 16-byte aligned, contents
+ * arbitrary, free again when the call's work is done.
+ * The FP8 form quantises nothing: A and sa are the base product's operands and
+ * X [M,K] (bf16) is what the adapters read.
+ * Constraints: the base calls' own (FP8: K <= 20480); K < 2^23; R % 8 == 0,
+ * R <= 4096, G <= 4096; M R, N R and G N R below 2^30 (La may be larger); X, La
+ * and Lb 16-byte aligned, ids and scale 4-byte.  R, G or K of 0: the base call.
  */
-int lora_shrink_bf16(const void *X, const void *La, const int32_t *ids, const float *scale, void *H,
-                     int M, int K, int R, int G, void *stream);
+long long lora_workspace(int M, int K, int R);
 
-int gemm_bf16_nt_lora(const void *A, const void *B, const void *H, const void *Lb, const int32_t *ids,
-                      void *D, int M, int N, int K, int R, int G, void *stream);
+int gemm_bf16_nt_lora(const void *A, const void *B, const void *La, const void *Lb, const int32_t *ids,
+                      const float *scale, void *D, void *ws, int M, int N, int K, int R, int G,
+                      void *stream);
 
 int gemm_fp8_1x128_128x128_bf16_lora(const void *A, const float *sa, const void *B, const float *sb,
-                                     const void *H, const void *Lb, const int32_t *ids, void *D, int M,
-                                     int N, int K, int R, int G, void *stream);
+                                     const void *X, const void *La, const void *Lb, const int32_t *ids,
+                                     const float *scale, void *D, void *ws, int M, int N, int K, int R,
+                                     int G, void *stream);
 
 #ifdef __cplusplus
 }

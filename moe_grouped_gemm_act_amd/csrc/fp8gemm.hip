@@ -57,7 +57,7 @@
 
 #include "e4m3.h"
 #include "fp8gemm.h"
-#include "fp8gemm_routed.h"
+#include "lora.h"
 
 namespace {
 
@@ -585,7 +585,7 @@ __device__ __forceinline__ void store_bf16(const v4f (&acc)[TN][TM], uint16_t *D
 
 // ---- low-rank adapters in the tile kernel ----------------------------------
 // Row m of a dense product adds h[m] Lb_a^T for its adapter a = ids[m], with
-// h[m] (lr values) formed before (lora_shrink_bf16).  A tile takes that sum as
+// h[m] (lr values) formed before (lora.hip).  A tile takes that sum as
 // more K blocks behind the base product's, into the same accumulators, so D is
 // rounded once and never read: with a_0 < a_1 < ... the adapters that the
 // tile's rows name, the added K axis is the ranks of a_0, then those of a_1,
@@ -2200,63 +2200,6 @@ int grouped_masked_bf16(const void *A, const void *B, void *D, int M, int N, int
   return launch_tile<1, 4, 8, 2, 4, 4, MASKED, false, false, true>(a, G, s);
 }
 
-// A product with adapters: the arguments beyond the base product's.  Returns
-// -1 where the base call alone is the answer.
-static int check_lora(const void *H, const void *Lb, const int32_t *ids, int M, int N, int K, int R,
-                      int G) {
-  if (R < 0 || G < 0) return FP8GEMM_INVALID_ARG;
-  if (M <= 0 || N <= 0 || K <= 0 || R == 0 || G == 0) return -1;
-  if (!H || !Lb || !ids) return FP8GEMM_INVALID_ARG;
-  if (R % 8 != 0 || G > LORA_MAXG || R > 4096) return FP8GEMM_UNSUPPORTED_SHAPE;
-  const long long lim = 1LL << 30;  // 2^31 bytes
-  if ((long long)M * R >= lim || (long long)N * R >= lim || (long long)G * N * R >= lim)
-    return FP8GEMM_UNSUPPORTED_SHAPE;
-  if (!aligned(H, 16) || !aligned(Lb, 16) || !aligned(ids, 4)) return FP8GEMM_MISALIGNED;
-  return FP8GEMM_OK;
-}
-
-int gemm_bf16_nt_lora(const void *A, const void *B, const void *H, const void *Lb, const int32_t *ids,
-                      void *D, int M, int N, int K, int R, int G, void *stream) {
-  const int sl = check_lora(H, Lb, ids, M, N, K, R, G);
-  if (sl < 0) return gemm_bf16_nt(A, B, D, M, N, K, stream);
-  if (sl != FP8GEMM_OK) return sl;
-  const int st = check_bf16(A, B, D, M, N, K, (long long)M * K, (long long)N * K,
-                            (long long)M * N);
-  if (st != FP8GEMM_OK) return st;
-  Args a{static_cast<const uint8_t *>(A), nullptr, static_cast<const uint8_t *>(B), nullptr,
-         static_cast<uint16_t *>(D), M, N, K, 1, nullptr, 0, 0, 1, 2 * K / BK, nullptr};
-  a.lh = static_cast<const uint16_t *>(H);
-  a.lb = static_cast<const uint16_t *>(Lb);
-  a.lids = ids;
-  a.lr = R;
-  a.lg = G;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  if (M <= 128) return run_decode<true, true>(a, s);
-  return launch_dense_large<2, 4, 4, 4, 3, 4, true, true>(a, s);
-}
-
-int gemm_fp8_1x128_128x128_bf16_lora(const void *A, const float *sa, const void *B, const float *sb,
-                                     const void *H, const void *Lb, const int32_t *ids, void *D, int M,
-                                     int N, int K, int R, int G, void *stream) {
-  const int sl = check_lora(H, Lb, ids, M, N, K, R, G);
-  if (sl < 0) return gemm_fp8_1x128_128x128_bf16(A, sa, B, sb, D, M, N, K, stream);
-  if (sl != FP8GEMM_OK) return sl;
-  const int st = check_common(A, sa, B, sb, D, M, N, K, (long long)M * K, (long long)N * K,
-                              (long long)M * N);
-  if (st != FP8GEMM_OK) return st;
-  if (K > 20480) return FP8GEMM_UNSUPPORTED_SHAPE;  // past the tile kernel's range
-  Args a{static_cast<const uint8_t *>(A), sa, static_cast<const uint8_t *>(B), sb,
-         static_cast<uint16_t *>(D), M, N, K, 1, nullptr, 0, 0, 1, K / BK, nullptr};
-  a.lh = static_cast<const uint16_t *>(H);
-  a.lb = static_cast<const uint16_t *>(Lb);
-  a.lids = ids;
-  a.lr = R;
-  a.lg = G;
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  if (M <= 128) return run_decode<false, true>(a, s);
-  return launch_dense_large<4, 2, 4, 4, 3, 4, false, true>(a, s);
-}
-
 const char *fp8gemm_status_string(int status) {
   switch (status) {
     case FP8GEMM_OK: return "ok";
@@ -2270,3 +2213,38 @@ const char *fp8gemm_status_string(int status) {
 }
 
 }  // extern "C"
+
+// ---- products with adapters ------------------------------------------------
+// The base product's arguments are checked as in its own call, then the
+// adapters'.
+int lora_product_check(const LoraProduct &p) {
+  if (p.R < 0 || p.G < 0) return FP8GEMM_INVALID_ARG;
+  const long long a = (long long)p.M * p.K, b = (long long)p.N * p.K, d = (long long)p.M * p.N;
+  const int st = p.fp8 ? check_common(p.A, p.sa, p.B, p.sb, p.D, p.M, p.N, p.K, a, b, d)
+                       : check_bf16(p.A, p.B, p.D, p.M, p.N, p.K, a, b, d);
+  if (st != FP8GEMM_OK) return st;
+  if (p.K == 0 || p.R == 0 || p.G == 0) return -1;
+  if (!p.H || !p.Lb || !p.ids) return FP8GEMM_INVALID_ARG;
+  if (p.R % 8 != 0 || p.G > LORA_MAXG || p.R > 4096 || (p.fp8 && p.K > 20480))
+    return FP8GEMM_UNSUPPORTED_SHAPE;
+  const long long lim = 1LL << 30;  // 2^31 bytes
+  if ((long long)p.M * p.R >= lim || (long long)p.N * p.R >= lim || (long long)p.G * p.N * p.R >= lim)
+    return FP8GEMM_UNSUPPORTED_SHAPE;
+  if (!aligned(p.H, 16) || !aligned(p.Lb, 16) || !aligned(p.ids, 4)) return FP8GEMM_MISALIGNED;
+  return FP8GEMM_OK;
+}
+
+int lora_product(const LoraProduct &p) {
+  Args a{static_cast<const uint8_t *>(p.A), p.sa, static_cast<const uint8_t *>(p.B), p.sb,
+         static_cast<uint16_t *>(p.D), p.M, p.N, p.K, 1, nullptr, 0, 0, 1,
+         (p.fp8 ? p.K : 2 * p.K) / BK, nullptr};
+  a.lh = static_cast<const uint16_t *>(p.H);
+  a.lb = static_cast<const uint16_t *>(p.Lb);
+  a.lids = p.ids;
+  a.lr = p.R;
+  a.lg = p.G;
+  hipStream_t s = static_cast<hipStream_t>(p.stream);
+  if (p.fp8)
+    return p.M <= 128 ? run_decode<false, true>(a, s) : launch_dense_large<4, 2, 4, 4, 3, 4, false, true>(a, s);
+  return p.M <= 128 ? run_decode<true, true>(a, s) : launch_dense_large<2, 4, 4, 4, 3, 4, true, true>(a, s);
+}

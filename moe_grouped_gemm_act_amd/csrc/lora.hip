@@ -1,13 +1,18 @@
-// First factor of the low-rank adapters for gfx950:
-//   H[m][r] = bf16(scale[a] sum_k X[m,k] La[a][r,k]),  a = ids[m].
+// Low-rank adapters beside a dense product for gfx950: the calls, and the
+// first factor's product
+//   H[m][r] = bf16(scale[a] sum_k X[m,k] La[a][r,k]),  a = ids[m],
+// which the tile kernel then takes as more K blocks (fp8gemm.hip).  H is
+// rounded to bf16 because it is a matrix instruction's operand there; the sums
+// before and after are fp32.
 //
-// Bound by reading X and the adapters in use once.  A workgroup takes 16 rows
-// of X, finds their distinct adapters and forms, for each of those it is
-// given, RT x 16 ranks for the rows that name it: its eight waves take the
-// 64-wide K blocks in turn (two 16x16x32 bf16 MFMAs per 16 ranks and block),
-// and their fp32 partial tiles meet in LDS, summed in wave order.  Rows of
-// other adapters are not loaded (zeros in the operand), so each row of X is
-// read once per RT x 16 ranks however the requests are mixed.
+// Bound by reading X and the adapters in use once.  Two forms:
+//   * few rows (decode, M R <= LORA_DOT): one wave per row and rank, a dot
+//     product along K with all of its 16-byte loads in flight at once.  Every
+//     row reads its adapter's factor itself, which costs nothing when the rows
+//     name different adapters and little while they are few.
+//   * more rows: 64 rows x RT 16 ranks a workgroup on the matrix cores, K
+//     split over workgroups until they fill the chip; the fp32 partial planes
+//     are summed in order by a second, small kernel.
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -16,104 +21,333 @@
 
 #include "bf16.h"
 #include "fp8gemm_routed.h"
+#include "lora.h"
 
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 
-constexpr int WAVES = 8, ROWS = 16;
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t rsrc(const void *p, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00020000);
+}
+constexpr uint32_t OOB = 0x80000000u;  // past any resource: reads zeros, moves nothing
+__device__ __forceinline__ u32x4 load16(__amdgpu_buffer_rsrc_t r, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t off, void *lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void *)lds, 16,
+                                           off, 0, 0, 0);
+}
+constexpr int vmcnt_imm(int n) { return (n & 15) | (((n >> 4) & 3) << 14) | 0x0F70; }
 
+// ---- few rows ----------------------------------------------------------------
+// Wave r of the grid's row m: U 16-byte pieces of X's row and of the adapter's
+// row a time (512 elements each over the wave); pieces past K read zeros.
+constexpr int DOT_WAVES = 4;
+
+template <int U>
+__global__ __launch_bounds__(DOT_WAVES * 64) void lora_dot_kernel(const uint16_t *X, const uint16_t *La,
+                                                                  const int32_t *ids, const float *scale,
+                                                                  uint16_t *H, int K, int R, int G) {
+  const int lane = threadIdx.x & 63;
+  const int m = blockIdx.y, r = blockIdx.x * DOT_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int ad = ids[m];
+  if (r >= R || ad < 0 || ad >= G) return;
+  const __amdgpu_buffer_rsrc_t rx = rsrc(X + (size_t)m * K, (uint32_t)K * 2);
+  const __amdgpu_buffer_rsrc_t rl = rsrc(La + ((size_t)ad * R + r) * K, (uint32_t)K * 2);
+  float acc[2] = {0.f, 0.f};
+  for (uint32_t k = lane * 16; k < (uint32_t)K * 2 + lane * 16; k += U * 1024) {
+    u32x4 x[U], l[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      x[u] = load16(rx, k + u * 1024);
+      l[u] = load16(rl, k + u * 1024);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        acc[0] = __builtin_fmaf(bf16_lo(x[u][e]), bf16_lo(l[u][e]), acc[0]);
+        acc[1] = __builtin_fmaf(bf16_hi(x[u][e]), bf16_hi(l[u][e]), acc[1]);
+      }
+  }
+  const float s = wave_sum(acc[0] + acc[1]);
+  if (lane == 0) H[(size_t)m * R + r] = (uint16_t)bf16_of(scale[ad] * s);
+}
+
+// ---- more rows ---------------------------------------------------------------
+// A workgroup lists its 64 rows' distinct adapters and takes a range of K
+// blocks (64 elements).  With few adapters its four waves share the blocks of
+// each adapter and their partial tiles meet in LDS; with WAVES or more, each
+// wave takes whole adapters.  Either way a wave feeds itself: direct-to-LDS
+// loads (8 rows x 128 bytes each, swizzled as the tile kernel's) into a ring of
+// its own, STAGES - 1 blocks ahead, with no barrier in the loop.  Rows of other
+// adapters are out-of-range loads: zeros, no traffic.
+constexpr int WAVES = 4, MT = 4, ROWS = MT * 16;
+constexpr int ring_stages(int rt) { return rt <= 2 ? 3 : 2; }  // 4 waves' rings within 144 KB
+
+__device__ __forceinline__ int row_key(int row) { return (row >> 1) & 7; }
+
+// dst: partial planes [gridDim.z][M][R] (fp32), or with one plane H itself
 template <int RT>
 __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t *X, const uint16_t *La,
                                                                  const int32_t *ids, const float *scale,
-                                                                 uint16_t *H, int M, int K, int R, int G) {
-  __shared__ v4f s_part[WAVES][RT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+                                                                 uint16_t *H, float *planes, int M, int K,
+                                                                 int R, int G, int tiles, int kb_per) {
+  constexpr int STAGES = ring_stages(RT);
+  constexpr int TR = (MT + RT) * 16, SLOT = TR * 128, PER = TR / 8;
+  static_assert(PER * STAGES < 64, "loads in flight must fit vmcnt");
+  static_assert(RT * MT * 1024 <= STAGES * SLOT, "partial tiles reuse the rings");
+  __shared__ __attribute__((aligned(1024))) uint8_t ring[WAVES][STAGES * SLOT];
+  __shared__ int s_id[ROWS], s_list[ROWS], s_n;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fg = lane >> 4;
-  const int m0 = blockIdx.x * ROWS, r0 = blockIdx.y * RT * 16;
-  // lanes fr, fr + 16, ... hold row fr's adapter; `first` marks the first row of each
-  int id = m0 + fr < M ? ids[m0 + fr] : -1;
-  if (id < 0 || id >= G) id = -1;
-  bool first = id >= 0;
+  // each XCD takes a run of consecutive row tiles, which often share adapters
+  const int x = blockIdx.x % 8, tile = x * (tiles / 8) + min(x, tiles % 8) + blockIdx.x / 8;
+  const int m0 = tile * ROWS, r0 = blockIdx.y * RT * 16;
+  if (wave == 0) {
+    int id = m0 + lane < M ? ids[m0 + lane] : -1;
+    if (id < 0 || id >= G) id = -1;
+    s_id[lane] = id;
+    bool first = id >= 0;  // the first row of its adapter
+    for (int i = 0; i < ROWS; ++i) {
+      const int other = (int)lane_of((uint32_t)id, i);
+      if (i < lane && other == id) first = false;
+    }
+    const unsigned long long b = __ballot(first);
+    if (first) s_list[__popcll(b & ((1ull << lane) - 1))] = id;
+    if (lane == 0) s_n = __popcll(b);
+  }
+  __syncthreads();
+  const int n = s_n, kb0 = blockIdx.z * kb_per, nkb = min(K / 64, kb0 + kb_per) - kb0;
+  const bool apart = n >= WAVES;  // waves take whole adapters
+  const int q0 = apart ? wave : 0, qs = apart ? WAVES : 1, t0 = apart ? 0 : wave, ts = apart ? 1 : WAVES;
+  const int steps = nkb > t0 ? (nkb - t0 + ts - 1) / ts : 0;  // blocks t0, t0 + ts, ... of an adapter
+  const __amdgpu_buffer_rsrc_t rx = rsrc(X + (size_t)m0 * K, (uint32_t)min(ROWS, M - m0) * K * 2);
+  __amdgpu_buffer_rsrc_t rl = rx;
+  const uint32_t col = (uint32_t)((lane & 7) ^ row_key(lane >> 3)) * 16;
+  uint32_t off[PER];
+  int pq = q0, ps = 0, slot_p = 0;  // the producer's adapter (place in the list), block and slot
+  auto aim = [&]() {                // the producer's addresses for adapter pq
+    const int ad = s_list[min(pq, ROWS - 1)];
+    if (pq < n) rl = rsrc(La + ((size_t)ad * R + r0) * K, (uint32_t)min(RT * 16, R - r0) * K * 2);
 #pragma unroll
-  for (int i = 0; i < ROWS; ++i) first = first && !(i < fr && (int)lane_of((uint32_t)id, i) == id);
-  unsigned todo = (unsigned)__ballot(first) & 0xFFFFu;
-  const u32x4 zero = {0, 0, 0, 0};
-  for (int n = 0; todo; todo &= todo - 1, ++n) {
-    if (n % gridDim.z != blockIdx.z) continue;
-    const int ad = __builtin_amdgcn_readlane(id, __builtin_ctz(todo));
-    const bool mine = id == ad;
-    const uint16_t *xp = X + (size_t)(m0 + fr) * K + fg * 8;
-    const uint16_t *lp = La + ((size_t)ad * R + r0 + fr) * K + fg * 8;
-    v4f acc[RT];
+    for (int i = 0; i < PER; ++i) {
+      const int r = i * 8 + (lane >> 3);
+      // row_key(r) = row_key(r % 8) ^ (4 if r / 8 is odd)
+      const uint32_t c = (i & 1) ? col ^ 64 : col;
+      if (i < MT * 2) off[i] = s_id[r] == ad ? (uint32_t)r * K * 2 + c : OOB;
+      else off[i] = (uint32_t)(r - ROWS) * K * 2 + c;
+    }
+  };
+  auto produce = [&]() {
+    const bool real = pq < n && ps < steps;
+    const uint32_t k = (uint32_t)(kb0 + t0 + ps * ts) * 128;
+    uint8_t *sl = ring[wave] + slot_p * SLOT;
 #pragma unroll
-    for (int i = 0; i < RT; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int k = wave * 64; k < K; k += WAVES * 64) {
-      u32x4 x[2], l[RT][2];
+    for (int i = 0; i < PER; ++i)
+      dma16(i < MT * 2 ? rx : rl, real ? off[i] + k : OOB, sl + i * 1024);
+    slot_p = slot_p + 1 == STAGES ? 0 : slot_p + 1;
+    ++ps;
+    // on to the next adapter without a gap, where no other wave takes part
+    if (apart && ps >= steps && pq < n) {
+      pq += qs;
+      ps = 0;
+      aim();
+    }
+  };
+  const int lo = fr * 128 + ((fg ^ row_key(fr)) << 4), hi = fr * 128 + (((fg + 4) ^ row_key(fr)) << 4);
+  int slot = 0;
+  for (int q = q0; q < n; q += qs) {
+    if (!apart || q == q0) {
+      pq = q;
+      ps = 0;
+      slot_p = slot = 0;
+      aim();
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        x[h] = mine ? *reinterpret_cast<const u32x4 *>(xp + k + h * 32) : zero;
+      for (int s = 0; s < STAGES - 1; ++s) produce();
+    }
+    v4f acc[RT][MT];
 #pragma unroll
-        for (int i = 0; i < RT; ++i)
-          l[i][h] = r0 + i * 16 + fr < R
-                        ? *reinterpret_cast<const u32x4 *>(lp + (size_t)i * 16 * K + k + h * 32)
-                        : zero;
+    for (int i = 0; i < RT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+    for (int s = 0; s < steps; ++s) {
+      __builtin_amdgcn_s_waitcnt(0xC07F);  // the last block's fragments are in registers: its slot is free
+      asm volatile("" ::: "memory");
+      produce();
+      __builtin_amdgcn_s_waitcnt(vmcnt_imm(PER * (STAGES - 1)));  // this block has landed
+      asm volatile("" ::: "memory");
+      const uint8_t *sl = ring[wave] + slot * SLOT;
+      bf16x8 a[MT][2], b[RT][2];
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        a[j][0] = *reinterpret_cast<const bf16x8 *>(sl + j * 2048 + lo);
+        a[j][1] = *reinterpret_cast<const bf16x8 *>(sl + j * 2048 + hi);
+      }
+#pragma unroll
+      for (int i = 0; i < RT; ++i) {
+        b[i][0] = *reinterpret_cast<const bf16x8 *>(sl + (MT + i) * 2048 + lo);
+        b[i][1] = *reinterpret_cast<const bf16x8 *>(sl + (MT + i) * 2048 + hi);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int i = 0; i < RT; ++i)
-          acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, l[i][h]),
-                                                           __builtin_bit_cast(bf16x8, x[h]), acc[i], 0, 0, 0);
+#pragma unroll
+          for (int j = 0; j < MT; ++j)
+            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i][h], a[j][h], acc[i][j], 0, 0, 0);
+      asm volatile("" ::: "memory");
+      slot = slot + 1 == STAGES ? 0 : slot + 1;
     }
-#pragma unroll
-    for (int i = 0; i < RT; ++i) s_part[wave][i][lane] = acc[i];
-    __syncthreads();
-    // wave i sums the i-th 16 ranks: lane holds row fr's ranks 4 fg .. 4 fg + 3
-    if (wave < RT) {
-      v4f s = s_part[0][wave][lane];
-#pragma unroll
-      for (int v = 1; v < WAVES; ++v) s += s_part[v][wave][lane];
-      const int r = r0 + wave * 16 + 4 * fg;
-      if (mine && r < R) {  // R is a multiple of 8
+    const int ad = s_list[q];
+    auto put = [&](const v4f &s, int i, int j) {  // ranks 4 fg .. 4 fg + 3 of the i-th 16, row fr of the j-th
+      const int r = r0 + i * 16 + 4 * fg, m = j * 16 + fr;
+      if (s_id[m] != ad || r >= R) return;  // R is a multiple of 8
+      const size_t at = (size_t)(m0 + m) * R + r;
+      if (gridDim.z > 1) {
+        *reinterpret_cast<v4f *>(planes + (size_t)blockIdx.z * M * R + at) = s;
+      } else {
         const float f = scale[ad];
-        *reinterpret_cast<u32x2 *>(H + (size_t)(m0 + fr) * R + r) =
-            u32x2{bf16_pair(f * s[0], f * s[1]), bf16_pair(f * s[2], f * s[3])};
+        *reinterpret_cast<u32x2 *>(H + at) = u32x2{bf16_pair(f * s[0], f * s[1]), bf16_pair(f * s[2], f * s[3])};
       }
+    };
+    if (apart) {
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) put(acc[i][j], i, j);
+    } else {
+      __builtin_amdgcn_s_waitcnt(0);  // nothing still lands in the ring, which the partial tiles reuse
+      v4f *part = reinterpret_cast<v4f *>(ring[wave]);
+#pragma unroll
+      for (int i = 0; i < RT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) part[(i * MT + j) * 64 + lane] = acc[i][j];
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < RT * MT / WAVES; ++e) {
+        const int p = wave * (RT * MT / WAVES) + e;
+        v4f s = reinterpret_cast<const v4f *>(ring[0])[p * 64 + lane];
+#pragma unroll
+        for (int v = 1; v < WAVES; ++v) s += reinterpret_cast<const v4f *>(ring[v])[p * 64 + lane];
+        put(s, p / MT, p % MT);
+      }
+      __syncthreads();  // all partial tiles read before the rings fill again
     }
-    __syncthreads();
   }
+  __builtin_amdgcn_s_waitcnt(0);  // nothing may still write LDS when the workgroup ends
+}
+
+// H from the partial planes, summed in order
+__global__ __launch_bounds__(256) void lora_join_kernel(const float *planes, const int32_t *ids,
+                                                        const float *scale, uint16_t *H, int M, int R, int G,
+                                                        int n) {
+  const long long q = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int m = (int)(q / (R / 4));
+  if (m >= M) return;
+  const int ad = ids[m];
+  if (ad < 0 || ad >= G) return;
+  const size_t plane = (size_t)M * R;
+  v4f s = *reinterpret_cast<const v4f *>(planes + q * 4);
+#pragma unroll 4
+  for (int i = 1; i < n; ++i) s += *reinterpret_cast<const v4f *>(planes + i * plane + q * 4);
+  const float f = scale[ad];
+  *reinterpret_cast<u32x2 *>(H + q * 4) = u32x2{bf16_pair(f * s[0], f * s[1]), bf16_pair(f * s[2], f * s[3])};
+}
+
+constexpr int LORA_DOT = 8192;  // rows x ranks up to which the dot form is used
+
+struct ShrinkPlan {
+  bool dot;
+  int rt, tiles, ry, planes, kb_per;
+};
+
+ShrinkPlan shrink_plan(int M, int K, int R) {
+  ShrinkPlan p{};
+  p.dot = (long long)M * R <= LORA_DOT;
+  p.rt = std::min(4, (R + 15) / 16);
+  p.tiles = (M + ROWS - 1) / ROWS;
+  p.ry = (R + p.rt * 16 - 1) / (p.rt * 16);
+  // K blocks shared out until 256 workgroups run, at least one block a wave
+  const int nkb = K / 64;
+  const int want = (int)std::max(1LL, 256LL / ((long long)p.tiles * p.ry));
+  p.planes = std::max(1, std::min(want, nkb / WAVES));
+  p.kb_per = nkb > 0 ? (nkb + p.planes - 1) / p.planes : 0;
+  p.planes = nkb > 0 ? (nkb + p.kb_per - 1) / p.kb_per : 1;
+  return p;
+}
+
+size_t h_bytes(int M, int R) { return ((size_t)M * R * 2 + 255) / 256 * 256; }
+
+int launch(const void *f, dim3 grid, int threads, void **args, void *stream) {
+  return hipLaunchKernel(f, grid, dim3(threads), args, 0, static_cast<hipStream_t>(stream)) == hipSuccess
+             ? FP8GEMM_OK
+             : FP8GEMM_LAUNCH_FAILED;
+}
+
+int shrink(const void *X, const void *La, const int32_t *ids, const float *scale, void *H, float *planes,
+           int M, int K, int R, int G, void *stream) {
+  ShrinkPlan p = shrink_plan(M, K, R);
+  if (p.dot) {
+    void *args[] = {&X, &La, &ids, &scale, &H, &K, &R, &G};
+    const void *f = K <= 2048   ? reinterpret_cast<const void *>(&lora_dot_kernel<4>)
+                    : K <= 4096 ? reinterpret_cast<const void *>(&lora_dot_kernel<8>)
+                                : reinterpret_cast<const void *>(&lora_dot_kernel<14>);
+    return launch(f, dim3((R + DOT_WAVES - 1) / DOT_WAVES, M), DOT_WAVES * 64, args, stream);
+  }
+  void *args[] = {&X, &La, &ids, &scale, &H, &planes, &M, &K, &R, &G, &p.tiles, &p.kb_per};
+  const void *f = p.rt == 1   ? reinterpret_cast<const void *>(&lora_shrink_kernel<1>)
+                  : p.rt == 2 ? reinterpret_cast<const void *>(&lora_shrink_kernel<2>)
+                  : p.rt == 3 ? reinterpret_cast<const void *>(&lora_shrink_kernel<3>)
+                              : reinterpret_cast<const void *>(&lora_shrink_kernel<4>);
+  const int st = launch(f, dim3(p.tiles, p.ry, p.planes), WAVES * 64, args, stream);
+  if (st != FP8GEMM_OK || p.planes == 1) return st;
+  void *jargs[] = {&planes, &ids, &scale, &H, &M, &R, &G, &p.planes};
+  return launch(reinterpret_cast<const void *>(&lora_join_kernel),
+                dim3((unsigned)(((long long)M * (R / 4) + 255) / 256)), 256, jargs, stream);
 }
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
+// every check, then the first factor's product and the whole
+int product(LoraProduct p, const void *X, const void *La, const float *scale, void *ws) {
+  p.H = ws;
+  const int st = lora_product_check(p);
+  if (st > 0) return st;
+  if (st < 0) return p.fp8 ? gemm_fp8_1x128_128x128_bf16(p.A, p.sa, p.B, p.sb, p.D, p.M, p.N, p.K, p.stream)
+                           : gemm_bf16_nt(p.A, p.B, p.D, p.M, p.N, p.K, p.stream);
+  if (!X || !La || !scale) return FP8GEMM_INVALID_ARG;
+  if (p.K >= 1 << 23) return FP8GEMM_UNSUPPORTED_SHAPE;
+  if (!aligned(X, 16) || !aligned(La, 16) || !aligned(scale, 4)) return FP8GEMM_MISALIGNED;
+  float *planes = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + h_bytes(p.M, p.R));
+  const int s2 = shrink(X, La, p.ids, scale, ws, planes, p.M, p.K, p.R, p.G, p.stream);
+  return s2 != FP8GEMM_OK ? s2 : lora_product(p);
+}
+
 }  // namespace
 
-extern "C" int lora_shrink_bf16(const void *X, const void *La, const int32_t *ids, const float *scale,
-                                void *H, int M, int K, int R, int G, void *stream) {
-  if (M < 0 || K < 0 || R < 0 || G < 0) return FP8GEMM_INVALID_ARG;
-  if (M == 0 || R == 0 || G == 0) return FP8GEMM_OK;
-  if (!ids || !scale || !H || (K > 0 && (!X || !La))) return FP8GEMM_INVALID_ARG;
-  if (K % 64 != 0 || R % 8 != 0 || R > 4096 || G > 4096 || (long long)M * R >= (1LL << 30))
-    return FP8GEMM_UNSUPPORTED_SHAPE;
-  if (!aligned(X, 16) || !aligned(La, 16) || !aligned(H, 16) || !aligned(ids, 4) || !aligned(scale, 4))
-    return FP8GEMM_MISALIGNED;
-  // Few row tiles: 16 ranks and one adapter a workgroup, so that the adapters'
-  // rows stream through many CUs; many: a workgroup takes its rows' adapters
-  // one after the other and 64 ranks at once, so X is read once.
-  const int tiles = (M + ROWS - 1) / ROWS, r16 = (R + 15) / 16;
-  const bool few = tiles < 64;
-  const int rt = few ? 1 : std::min(4, r16);
-  const int z = few ? ROWS : 1;
-  const dim3 grid(tiles, (r16 + rt - 1) / rt, z);
-  void *args[] = {&X, &La, &ids, &scale, &H, &M, &K, &R, &G};
-  const void *f = rt == 1   ? reinterpret_cast<const void *>(&lora_shrink_kernel<1>)
-                  : rt == 2 ? reinterpret_cast<const void *>(&lora_shrink_kernel<2>)
-                  : rt == 3 ? reinterpret_cast<const void *>(&lora_shrink_kernel<3>)
-                            : reinterpret_cast<const void *>(&lora_shrink_kernel<4>);
-  return hipLaunchKernel(f, grid, dim3(WAVES * 64), args, 0, static_cast<hipStream_t>(stream)) ==
-                 hipSuccess
-             ? FP8GEMM_OK
-             : FP8GEMM_LAUNCH_FAILED;
+extern "C" {
+
+long long lora_workspace(int M, int K, int R) {
+  if (M <= 0 || K <= 0 || R <= 0) return 0;
+  const ShrinkPlan p = shrink_plan(M, K, R);
+  return (long long)(h_bytes(M, R) + (p.dot || p.planes == 1 ? 0 : (size_t)p.planes * M * R * 4));
 }
+
+int gemm_bf16_nt_lora(const void *A, const void *B, const void *La, const void *Lb, const int32_t *ids,
+                      const float *scale, void *D, void *ws, int M, int N, int K, int R, int G,
+                      void *stream) {
+  return product({A, nullptr, B, nullptr, nullptr, Lb, ids, D, M, N, K, R, G, false, stream}, A, La, scale, ws);
+}
+
+int gemm_fp8_1x128_128x128_bf16_lora(const void *A, const float *sa, const void *B, const float *sb,
+                                     const void *X, const void *La, const void *Lb, const int32_t *ids,
+                                     const float *scale, void *D, void *ws, int M, int N, int K, int R,
+                                     int G, void *stream) {
+  return product({A, sa, B, sb, nullptr, Lb, ids, D, M, N, K, R, G, true, stream}, X, La, scale, ws);
+}
+
+}  // extern "C"

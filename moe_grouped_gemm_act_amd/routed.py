@@ -27,7 +27,7 @@ ROUTED_HEADER = os.path.join(os.path.dirname(HEADER), "fp8gemm_routed.h")
 
 __all__ = ["moe_topk", "moe_topk_backward", "moe_contiguous_rows", "moe_sort_contiguous",
            "moe_sort_masked", "moe_dispatch_bf16", "moe_dispatch_fp8", "moe_dispatch_backward",
-           "moe_combine", "moe_combine_backward", "lora_shrink_bf16", "gemm_bf16_nt_lora",
+           "moe_combine", "moe_combine_backward", "gemm_bf16_nt_lora",
            "gemm_fp8_1x128_128x128_bf16_lora"]
 
 _routed = None
@@ -51,11 +51,11 @@ def _load():
                 ("moe_dispatch_fp8", [vp] * 4 + [i32] * 5 + [vp]),
                 ("moe_combine_bf16", [vp] * 4 + [i32] * 4 + [vp]),
                 ("moe_combine_backward_bf16", [vp] * 6 + [i32] * 4 + [vp]),
-                ("lora_shrink_bf16", [vp] * 5 + [i32] * 4 + [vp]),
-                ("gemm_bf16_nt_lora", [vp] * 6 + [i32] * 5 + [vp]),
-                ("gemm_fp8_1x128_128x128_bf16_lora", [vp] * 8 + [i32] * 5 + [vp])):
+                ("gemm_bf16_nt_lora", [vp] * 8 + [i32] * 5 + [vp]),
+                ("gemm_fp8_1x128_128x128_bf16_lora", [vp] * 11 + [i32] * 5 + [vp])):
             f = getattr(lib, name)
             f.argtypes, f.restype = args, i32
+        lib.lora_workspace.argtypes, lib.lora_workspace.restype = [i32] * 3, ctypes.c_longlong
         _routed = lib
     return _routed
 
@@ -249,53 +249,37 @@ def moe_combine_backward(dout, Y, row, w, dY=None, dw=None, stream=None):
     return dY, dw
 
 
-def lora_shrink_bf16(X, La, ids, scale, H=None, stream=None):
-    """H [M,R] (bfloat16) = scale[a] X[m] La[a]^T for each row's adapter
-    a = ids[m]: X [M,K] and La [G,R,K] bfloat16, ids [M] int32 (outside [0,G):
-    no adapter, H's row keeps its contents), scale [G] float32."""
-    M, K = X.shape
+def _adapters(base, X, M, K, N, La, Lb, ids, scale, D, stream):
+    """Checks the adapters' tensors and where all are; (R, G, device, workspace)."""
     G, R = La.shape[:2]
+    _shape(_typed(X, torch.bfloat16, "X"), (M, K), "X")
     _shape(_typed(La, torch.bfloat16, "La"), (G, R, K), "La")
+    _shape(_typed(Lb, torch.bfloat16, "Lb"), (G, N, R), "Lb")
     _shape(_typed(ids, torch.int32, "ids"), (M,), "ids")
     _shape(_typed(scale, torch.float32, "scale"), (G,), "scale")
-    H = _out(H, (M, R), torch.bfloat16, X.device, "H")
-    dev = _dev(_typed(X, torch.bfloat16, "X"), La, ids, scale, H)
-    _check(_load().lora_shrink_bf16(_p(X), _p(La), _p(ids), _p(scale), _p(H), M, K, R, G,
-                                    _stream(stream, dev)))
-    return H
+    dev = _dev(*base, X, La, Lb, ids, scale, D)
+    ws = torch.empty(_load().lora_workspace(M, K, R), dtype=torch.uint8, device=D.device)
+    if stream is not None:
+        ws.record_stream(stream)  # freed on return; the caching allocator waits for that stream
+    return R, G, dev, ws
 
 
-def _ranks(X, La, Lb, N, ids, scale, H, stream):
-    """H = lora_shrink_bf16(X, ...) and (R, G) for a product of N columns."""
-    G, R = La.shape[:2]
-    _shape(_typed(Lb, torch.bfloat16, "Lb"), (G, N, R), "Lb")
-    _dev(X, Lb)
-    given = H is not None
-    H = lora_shrink_bf16(X, La, ids, scale, H, stream)
-    if not given and stream is not None:
-        H.record_stream(stream)  # freed on return; the caching allocator waits for that stream
-    return H, R, G
-
-
-def gemm_bf16_nt_lora(A, B, La, Lb, ids, scale, D=None, H=None, stream=None):
+def gemm_bf16_nt_lora(A, B, La, Lb, ids, scale, D=None, stream=None):
     """gemm_bf16_nt with a low-rank adapter per row:
     D[m] = bf16(A[m] B^T + scale[a] (A[m] La[a]^T) Lb[a]^T), a = ids[m].
     A [M,K], B [N,K], La [G,R,K], Lb [G,N,R] bfloat16, ids [M] int32 (outside
-    [0,G): the base product alone), scale [G] float32.  H [M,R] (bfloat16)
-    keeps the first factor's product and may be given."""
+    [0,G): the base product alone), scale [G] float32."""
     M, K = A.shape
     N = B.shape[0]
     _shape(_typed(B, torch.bfloat16, "B"), (N, K), "B")
     D = _out(D, (M, N), torch.bfloat16, A.device, "D")
-    dev = _dev(A, B, D)
-    H, R, G = _ranks(A, La, Lb, N, ids, scale, H, stream)
-    _check(_load().gemm_bf16_nt_lora(_p(A), _p(B), _p(H), _p(Lb), _p(ids), _p(D), M, N, K, R, G,
-                                     _stream(stream, dev)))
+    R, G, dev, ws = _adapters((A, B), A, M, K, N, La, Lb, ids, scale, D, stream)
+    _check(_load().gemm_bf16_nt_lora(_p(A), _p(B), _p(La), _p(Lb), _p(ids), _p(scale), _p(D), _p(ws),
+                                     M, N, K, R, G, _stream(stream, dev)))
     return D
 
 
-def gemm_fp8_1x128_128x128_bf16_lora(A, sa, B, sb, X, La, Lb, ids, scale, D=None, H=None,
-                                     stream=None):
+def gemm_fp8_1x128_128x128_bf16_lora(A, sa, B, sb, X, La, Lb, ids, scale, D=None, stream=None):
     """gemm_fp8_1x128_128x128_bf16 with a low-rank adapter per row, which
     reads the unquantised X [M,K] (bfloat16): D[m] = bf16((block-scaled A B^T)[m]
     + scale[a] (X[m] La[a]^T) Lb[a]^T); the others as in gemm_bf16_nt_lora."""
@@ -305,11 +289,9 @@ def gemm_fp8_1x128_128x128_bf16_lora(A, sa, B, sb, X, La, Lb, ids, scale, D=None
     _shape(B, (N, K), "B")
     _shape(_typed(sa, torch.float32, "sa"), (K // 128, M), "sa")
     _shape(_typed(sb, torch.float32, "sb"), ((N + 127) // 128, K // 128), "sb")
-    _shape(X, (M, K), "X")
     D = _out(D, (M, N), torch.bfloat16, A.device, "D")
-    dev = _dev(A, sa, B, sb, X, D)
-    H, R, G = _ranks(X, La, Lb, N, ids, scale, H, stream)
+    R, G, dev, ws = _adapters((A, sa, B, sb), X, M, K, N, La, Lb, ids, scale, D, stream)
     _check(_load().gemm_fp8_1x128_128x128_bf16_lora(
-        _p(A), _p(sa), _p(B), _p(sb), _p(H), _p(Lb), _p(ids), _p(D), M, N, K, R, G,
-        _stream(stream, dev)))
+        _p(A), _p(sa), _p(B), _p(sb), _p(X), _p(La), _p(Lb), _p(ids), _p(scale), _p(D), _p(ws),
+        M, N, K, R, G, _stream(stream, dev)))
     return D

@@ -68,19 +68,18 @@ class Case:
         X, t = self.X.to(DEV), torch.from_numpy
         rest = (La.to(DEV), Lb.to(DEV), t(self.ids).to(DEV), t(self.scale).to(DEV))
         D = sentinel_out((self.M, self.N))
-        H = torch.full((self.M, self.R), float("nan"), dtype=torch.bfloat16, device=DEV)
-        kw = {"D": D, "H": H, **kw}
+        kw = {"D": D, **kw}
         if self.fp8:
             out = fg.gemm_fp8_1x128_128x128_bf16_lora(*self.ops, X, *rest, **kw)
         else:
             out = fg.gemm_bf16_nt_lora(X, *self.ops, *rest, **kw)
         torch.cuda.synchronize()
-        return out, H
+        return out
 
-    def check(self, D, H, Lb=None):
+    def check(self, D, Lb=None):
         Lb = self.Lb if Lb is None else Lb
         with np.errstate(invalid="ignore", over="ignore"):
-            want, mag, h = ref.lora(self.base, self.X.double().numpy(), self.La.double().numpy(), Lb.double().numpy(),
+            want, mag, _ = ref.lora(self.base, self.X.double().numpy(), self.La.double().numpy(), Lb.double().numpy(),
                                     self.ids, self.scale)
             got = D.double().cpu().numpy()
             n = self.K + self.R + 16
@@ -91,8 +90,6 @@ class Case:
             for m, a in enumerate(self.ids):
                 if 0 <= a < self.G:
                     he = self.K * U * self.scale[a] * xm[m, a]
-                    hb = 2.0 ** -8 * np.abs(h[m]) + he
-                    assert (np.abs(H[m].double().cpu().numpy() - h[m]) <= hb + 2.0 ** -133).all(), f"H row {m}"
                     bound[m] += np.abs(Lb[a].double().numpy()) @ he
             if self.fp8:
                 bound += 2.0 ** -12 * self.base_mag
@@ -107,6 +104,7 @@ SHAPES = [  # M, N, K, R, G
     (1, 64, 128, 8, 1), (1, 2112, 1024, 16, 4), (3, 97, 256, 24, 2), (17, 130, 128, 8, 40), (63, 576, 384, 64, 64),
     (64, 4096, 2048, 16, 64), (64, 24576, 256, 8, 5), (65, 1000, 640, 72, 9), (128, 4096, 1024, 32, 128),
     (128, 24600, 128, 16, 33), (129, 257, 256, 16, 7), (300, 1030, 512, 40, 3), (515, 2112, 384, 128, 12),
+    (200, 150, 960, 64, 3), (257, 300, 7168, 48, 2), (600, 70, 2048, 16, 300), (150, 64, 1024, 200, 5),
     (1100, 3700, 256, 64, 4096),
 ]
 
@@ -119,12 +117,11 @@ def test_product_with_adapters(M, N, K, R, G, fp8, how):
         pytest.skip("the largest adapter count is run once")
     if G == 4096:
         N, R = 61, 8
+    if fp8:
+        K = K // 128 * 128
     announce(f"lora M={M} N={N} K={K} R={R} G={G} fp8={fp8} {how}")
     c = Case(9000 + M + N + K + R, M, N, K, R, G, how, fp8)
-    D, H = c.run()
-    c.check(D, H)
-    unnamed = ~((c.ids >= 0) & (c.ids < G))
-    assert H.cpu()[torch.from_numpy(unnamed)].isnan().all()  # rows without an adapter are not written
+    c.check(c.run())
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -136,7 +133,7 @@ def test_few_base_blocks(K, fp8):
     for M in (5, 100, 200):
         announce(f"lora few blocks M={M} K={K} fp8={fp8}")
         c = Case(9100 + M + K, M, 200, K, 16, 30, "random", fp8)
-        c.check(*c.run())
+        c.check(c.run())
 
 
 @pytest.mark.parametrize("fp8", [False, True])
@@ -148,19 +145,18 @@ def test_an_adapter_with_nan_and_inf_reaches_its_own_rows_alone(M, N, fp8):
     Lb[2, ::7, 3] = float("nan")
     Lb[2, 1::7, 20] = float("inf")
     Lb[4, 5, 0] = -float("inf")
-    D, H = c.run(Lb=Lb)
+    D = c.run(Lb=Lb)
     assert D.isnan().any() and D.isinf().any()
-    c.check(D, H, Lb)
+    c.check(D, Lb)
 
 
 def test_a_row_with_nan_and_inf_reaches_itself_alone():
     c = Case(9300, 70, 200, 256, 16, 5, "random", False)
-    clean, _ = c.run()
     c.ids[[7, 33]] = 1
-    clean, _ = c.run()
+    clean = c.run()
     c.X[7, 5] = float("nan")
     c.X[33, 9] = float("inf")
-    D, _ = c.run()
+    D = c.run()
     other = [m for m in range(70) if m not in (7, 33)]
     assert torch.equal(D[other], clean[other])
     assert D[7].isnan().all() and not D[33].isfinite().any()
@@ -170,16 +166,16 @@ def test_a_row_with_nan_and_inf_reaches_itself_alone():
 def test_without_adapters_it_is_the_base_product(fp8):
     for M, N, K in ((64, 2112, 1024), (300, 700, 512)):
         c = Case(9400 + M, M, N, K, 16, 4, "none", fp8)
-        D, _ = c.run()
+        D = c.run()
         base = fg.gemm_fp8_1x128_128x128_bf16(*c.ops) if fp8 else fg.gemm_bf16_nt(c.X.to(DEV), *c.ops)
         assert torch.equal(D, base)
         # R = 0 and G = 0 are the base call
         none = torch.empty((4, 0, K), dtype=torch.bfloat16), torch.empty((4, N, 0), dtype=torch.bfloat16)
         c.R = 0
-        assert torch.equal(c.run(*none)[0], base)
+        assert torch.equal(c.run(*none), base)
         c.R, c.G, c.scale = 16, 0, c.scale[:0]
         none = torch.empty((0, 16, K), dtype=torch.bfloat16), torch.empty((0, N, 16), dtype=torch.bfloat16)
-        assert torch.equal(c.run(*none)[0], base)
+        assert torch.equal(c.run(*none), base)
 
 
 def test_zero_sizes():
@@ -196,7 +192,7 @@ def test_deterministic_and_independent_of_the_batch():
     """the same bits every time; and a row's bits do not depend on which other
     adapters its tile holds (decode, one K split plan)"""
     c = Case(9500, 64, 4096, 2048, 16, 64, "random", False)
-    a, b = c.run()[0].clone(), c.run()[0]
+    a, b = c.run().clone(), c.run()
     assert torch.equal(a, b)
 
 
@@ -218,7 +214,7 @@ def test_streams_and_graph_replay():
         s = torch.cuda.Stream()
         D.zero_()
         torch.cuda.synchronize()
-        call(stream=s)  # a temporary H, used on a stream that is not the current one
+        call(stream=s)  # a temporary workspace, used on a stream that is not the current one
         junk = torch.full((M, 16), float("nan"), dtype=torch.bfloat16, device=DEV)
         s.synchronize()
         assert torch.equal(D, eager)
@@ -245,15 +241,15 @@ def test_earlier_hip_error_is_not_reported():
         pytest.skip(f"HIP runtimes loaded: {sorted(paths)}")
     hip = ctypes.CDLL(paths.pop())
     c = Case(9700, 20, 256, 256, 16, 4, "random", False)
-    want = c.run()[0].clone()
+    want = c.run().clone()
     X, t = c.X.to(DEV), torch.from_numpy
     args = (X, *c.ops, c.La.to(DEV), c.Lb.to(DEV), t(c.ids).to(DEV), t(c.scale).to(DEV))
-    D, H = sentinel_out((20, 256)), torch.zeros((20, 16), dtype=torch.bfloat16, device=DEV)
+    D = sentinel_out((20, 256))
     torch.cuda.synchronize()
     p = ctypes.c_void_p()
     assert hip.hipMalloc(ctypes.byref(p), ctypes.c_size_t(1 << 62)) != 0
     try:
-        fg.gemm_bf16_nt_lora(*args, D=D, H=H)
+        fg.gemm_bf16_nt_lora(*args, D=D)
     finally:
         hip.hipGetLastError()
     torch.cuda.synchronize()

@@ -27,7 +27,7 @@ def lib():
 
 def test_exports_every_declared_function(lib):
     text = re.sub(r"/\*.*?\*/", "", open(routed.ROUTED_HEADER).read(), flags=re.S)
-    names = re.findall(r"^\s*int\s+(\w+)\s*\(", text, flags=re.M)
+    names = re.findall(r"^\s*(?:int|long long)\s+(\w+)\s*\(", text, flags=re.M)
     assert len(names) >= 12
     for n in names:
         assert hasattr(lib, n), n
@@ -191,31 +191,29 @@ def test_combine_validation(lib):
 
 
 def test_lora_validation(lib):
-    def shrink(X=P, La=P, ids=P, scale=P, H=Q, M=4, K=128, R=16, G=2):
-        return lib.lora_shrink_bf16(X, La, ids, scale, H, M, K, R, G, NUL)
+    def bf16(A=P, B=P, La=P, Lb=P, ids=P, scale=P, D=Q, ws=P, M=4, N=64, K=128, R=16, G=2):
+        return lib.gemm_bf16_nt_lora(A, B, La, Lb, ids, scale, D, ws, M, N, K, R, G, NUL)
 
-    def bf16(A=P, B=P, H=P, Lb=P, ids=P, D=Q, M=4, N=64, K=128, R=16, G=2):
-        return lib.gemm_bf16_nt_lora(A, B, H, Lb, ids, D, M, N, K, R, G, NUL)
-
-    def fp8(A=P, sa=P, B=P, sb=P, H=P, Lb=P, ids=P, D=Q, M=4, N=64, K=128, R=16, G=2):
-        return lib.gemm_fp8_1x128_128x128_bf16_lora(A, sa, B, sb, H, Lb, ids, D, M, N, K, R, G, NUL)
-    for call in (shrink, bf16, fp8):
-        assert call(M=-1) == call(K=-128) == call(R=-8) == call(G=-1) == INVALID
-        assert call(H=NUL) == call(ids=NUL) == INVALID
-        assert call(K=100) == call(R=12) == call(R=4104) == call(G=4097) == SHAPE
-        assert call(M=1 << 27, R=16) == SHAPE
-        assert call(H=P_ODD) == call(ids=P_BAD) == MISALIGNED
-    assert shrink(X=NUL) == shrink(La=NUL) == shrink(scale=NUL) == INVALID
-    assert shrink(X=P_ODD) == shrink(La=P_ODD) == shrink(scale=P_BAD) == MISALIGNED
-    assert shrink(NUL, NUL, NUL, NUL, NUL, M=0) == shrink(NUL, NUL, NUL, NUL, NUL, R=0) == OK
+    def fp8(A=P, sa=P, B=P, sb=P, X=P, La=P, Lb=P, ids=P, scale=P, D=Q, ws=P, M=4, N=64, K=128, R=16, G=2):
+        return lib.gemm_fp8_1x128_128x128_bf16_lora(A, sa, B, sb, X, La, Lb, ids, scale, D, ws, M, N, K, R, G, NUL)
     for call in (bf16, fp8):
-        assert call(N=-1) == call(Lb=NUL) == call(A=NUL) == call(B=NUL) == call(D=NUL) == INVALID
-        assert call(N=1 << 20, G=4096) == SHAPE
-        assert call(Lb=P_ODD) == call(A=P_ODD) == call(D=P_ODD) == MISALIGNED
-        assert call(M=0, A=NUL, B=NUL, H=NUL, Lb=NUL, ids=NUL, D=NUL) == OK
-        assert call(R=0, H=NUL, Lb=NUL, A=NUL) == INVALID  # the base call's own check
-    assert fp8(sa=NUL) == INVALID
+        assert call(M=-1) == call(N=-1) == call(K=-128) == call(R=-8) == call(G=-1) == INVALID
+        for name in ("A", "B", "La", "Lb", "ids", "scale", "D", "ws"):
+            assert call(**{name: NUL}) == INVALID, name
+        assert call(K=100) == call(R=12) == call(R=4104) == call(G=4097) == SHAPE
+        assert call(M=1 << 23, K=128, R=128) == call(N=1 << 20, G=4096) == SHAPE
+        for name in ("A", "B", "La", "Lb", "D", "ws"):
+            assert call(**{name: P_ODD}) == MISALIGNED, name
+        assert call(ids=P_BAD) == call(scale=P_BAD) == MISALIGNED
+        assert call(M=0, A=NUL, B=NUL, La=NUL, Lb=NUL, ids=NUL, scale=NUL, D=NUL, ws=NUL) == OK
+        assert call(R=0, Lb=NUL, A=NUL) == INVALID  # the base call's own check
+    assert bf16(K=1 << 23, M=1, N=1, R=8) == SHAPE
+    assert fp8(sa=NUL) == fp8(X=NUL) == INVALID
+    assert fp8(X=P_ODD) == MISALIGNED
     assert fp8(K=20608) == SHAPE
+    assert lib.lora_workspace(0, 128, 16) == lib.lora_workspace(4, 128, 0) == 0
+    assert lib.lora_workspace(4, 128, 16) >= 4 * 16 * 2
+    assert lib.lora_workspace(4096, 7168, 64) > 4096 * 64 * 2
 
 
 def test_lora_reference_is_the_dense_sum():
@@ -254,4 +252,4 @@ def test_binding_refusals():
         with pytest.raises(ValueError):
             fg.gemm_bf16_nt_lora(*bad)
     with pytest.raises(TypeError):
-        fg.lora_shrink_bf16(x, La.float(), ids, scale)
+        fg.gemm_bf16_nt_lora(x, W, La.float(), Lb, ids, scale)
