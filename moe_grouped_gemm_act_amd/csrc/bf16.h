@@ -53,3 +53,16 @@ static __device__ __forceinline__ float wave_sum(float f) {
   return (__uint_as_float(lane_of(u, 0)) + __uint_as_float(lane_of(u, 16))) +
          (__uint_as_float(lane_of(u, 32)) + __uint_as_float(lane_of(u, 48)));
 }
+
+// Whether bf16 values seen in pairs are all finite: the greatest magnitude in
+// each half, as an integer (infinities and NaN have exponents of all ones).
+struct bf16_peak {
+  typedef unsigned short us2 __attribute__((ext_vector_type(2)));
+  us2 top = {0, 0};
+  __device__ __forceinline__ void see(u32x4 v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      top = __builtin_elementwise_max(top, __builtin_bit_cast(us2, (uint32_t)(v[i] & 0x7FFF7FFFu)));
+  }
+  __device__ __forceinline__ bool finite() const { return top[0] < 0x7F80 && top[1] < 0x7F80; }
+};

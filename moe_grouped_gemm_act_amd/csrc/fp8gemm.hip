@@ -55,6 +55,7 @@
 #include <mutex>
 #include <vector>
 
+#include "bf16.h"
 #include "e4m3.h"
 #include "fp8gemm.h"
 #include "lora.h"
@@ -63,8 +64,6 @@ namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int BK = 128;        // K block = one scale block = one MFMA's K
 constexpr int THREADS = 256;   // 4 waves of 64
@@ -639,16 +638,16 @@ __device__ __forceinline__ void adapter_kblock(const uint8_t *sl, int e0, int R,
   const int lo = fr * BK + chunk_pos(fg, fr), hi = fr * BK + chunk_pos(fg + 4, fr);
   const uint8_t *pa = sl + wm * TM * 16 * BK, *pb = sl + (BM + wn * TN * 16) * BK;
   constexpr int G = 16 * BK;  // bytes per 16-row group
-  unsigned wild = 0;  // a bf16 exponent of all ones in the low or high half of any word
+  bf16_peak peak;
   {
     v8i bfr[TN];
 #pragma unroll
     for (int i = 0; i < TN; ++i) {
       bfr[i] = frag_at(pb + i * G + lo, pb + i * G + hi);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) wild |= (((bfr[i][e] & 0x7F807F80u) >> 7) + 0x00010001u) & 0x01000100u;
+      peak.see(__builtin_bit_cast(u32x4, bf_half(bfr[i], 0)));
+      peak.see(__builtin_bit_cast(u32x4, bf_half(bfr[i], 1)));
     }
-    if (__ballot(wild != 0) == 0) {
+    if (__ballot(!peak.finite()) == 0) {
 #pragma unroll
       for (int j = 0; j < TM; ++j) {
         asm volatile("" ::: "memory");  // one activation fragment at a time

@@ -78,11 +78,14 @@ __global__ __launch_bounds__(DOT_WAVES * 64) void lora_dot_kernel(const uint16_t
 
 // ---- more rows ---------------------------------------------------------------
 // A workgroup lists its 64 rows' distinct adapters and takes a range of K
-// blocks (64 elements).  With few adapters its four waves share the blocks of
-// each adapter and their partial tiles meet in LDS; with WAVES or more, each
-// wave takes whole adapters.  Either way a wave feeds itself: direct-to-LDS
-// loads (8 rows x 128 bytes each, swizzled as the tile kernel's) into a ring of
-// its own, STAGES - 1 blocks ahead, with no barrier in the loop.  Rows of other
+// blocks (64 elements).  Its work is the sequence of all (adapter, block)
+// pairs, which its four waves take in turn.  A row is zero in the blocks of
+// every adapter but its own, so all of them add into the same accumulators and
+// the waves' partial tiles meet once, in LDS, at the end.  (Zero times an
+// infinite or NaN weight would reach other adapters' rows: a block that holds
+// one adds to its own rows alone.)  A wave feeds itself: direct-to-LDS loads (8
+// rows x 128 bytes each, swizzled as the tile kernel's) into a ring of its own,
+// STAGES - 1 blocks ahead, with no barrier in the loop.  Rows of other
 // adapters are out-of-range loads: zeros, no traffic.
 constexpr int WAVES = 4, MT = 4, ROWS = MT * 16;
 constexpr int ring_stages(int rt) { return rt <= 2 ? 3 : 2; }  // 4 waves' rings within 144 KB
@@ -111,87 +114,85 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
     int id = m0 + lane < M ? ids[m0 + lane] : -1;
     if (id < 0 || id >= G) id = -1;
     s_id[lane] = id;
-    bool first = id >= 0;  // the first row of its adapter
-    for (int i = 0; i < ROWS; ++i) {
-      const int other = (int)lane_of((uint32_t)id, i);
-      if (i < lane && other == id) first = false;
+    unsigned long long rest = __ballot(id >= 0);
+    int n = 0;
+    while (rest) {  // one turn per distinct adapter
+      const int ad = (int)lane_of((uint32_t)id, __builtin_ctzll(rest));
+      if (lane == 0) s_list[n] = ad;
+      ++n;
+      rest &= ~__ballot(id == ad);
     }
-    const unsigned long long b = __ballot(first);
-    if (first) s_list[__popcll(b & ((1ull << lane) - 1))] = id;
-    if (lane == 0) s_n = __popcll(b);
+    if (lane == 0) s_n = n;
   }
   __syncthreads();
   const int n = s_n, kb0 = blockIdx.z * kb_per, nkb = min(K / 64, kb0 + kb_per) - kb0;
-  const bool apart = n >= WAVES;  // waves take whole adapters
-  const int q0 = apart ? wave : 0, qs = apart ? WAVES : 1, t0 = apart ? 0 : wave, ts = apart ? 1 : WAVES;
-  const int steps = nkb > t0 ? (nkb - t0 + ts - 1) / ts : 0;  // blocks t0, t0 + ts, ... of an adapter
+  if (n == 0) return;
   const __amdgpu_buffer_rsrc_t rx = rsrc(X + (size_t)m0 * K, (uint32_t)min(ROWS, M - m0) * K * 2);
   __amdgpu_buffer_rsrc_t rl = rx;
   const uint32_t col = (uint32_t)((lane & 7) ^ row_key(lane >> 3)) * 16;
   uint32_t off[PER];
-  int pq = q0, ps = 0, slot_p = 0;  // the producer's adapter (place in the list), block and slot
-  auto aim = [&]() {                // the producer's addresses for adapter pq
-    const int ad = s_list[min(pq, ROWS - 1)];
-    if (pq < n) rl = rsrc(La + ((size_t)ad * R + r0) * K, (uint32_t)min(RT * 16, R - r0) * K * 2);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
+  for (int i = MT * 2; i < PER; ++i)  // row_key(r) = row_key(r % 8) ^ 4 where r / 8 is odd
+    off[i] = (uint32_t)(i * 8 + (lane >> 3) - ROWS) * K * 2 + ((i & 1) ? col ^ 64 : col);
+  int pq = 0, pk = wave, pslot = 0;  // the producer's adapter (place in the list), block and slot
+  auto aim = [&]() {                 // its addresses for a new adapter
+    while (pk >= nkb && pq < n) {
+      pk -= nkb;
+      ++pq;
+    }
+    if (pq >= n) return;
+    const int ad = s_list[pq];
+    rl = rsrc(La + ((size_t)ad * R + r0) * K, (uint32_t)min(RT * 16, R - r0) * K * 2);
+#pragma unroll
+    for (int i = 0; i < MT * 2; ++i) {
       const int r = i * 8 + (lane >> 3);
-      // row_key(r) = row_key(r % 8) ^ (4 if r / 8 is odd)
-      const uint32_t c = (i & 1) ? col ^ 64 : col;
-      if (i < MT * 2) off[i] = s_id[r] == ad ? (uint32_t)r * K * 2 + c : OOB;
-      else off[i] = (uint32_t)(r - ROWS) * K * 2 + c;
+      off[i] = s_id[r] == ad ? (uint32_t)r * K * 2 + ((i & 1) ? col ^ 64 : col) : OOB;
     }
   };
-  auto produce = [&]() {
-    const bool real = pq < n && ps < steps;
-    const uint32_t k = (uint32_t)(kb0 + t0 + ps * ts) * 128;
-    uint8_t *sl = ring[wave] + slot_p * SLOT;
+  auto produce = [&]() {  // past the last pair: nothing is loaded
+    const bool real = pq < n;
+    const uint32_t k = (uint32_t)(kb0 + pk) * 128;
+    uint8_t *sl = ring[wave] + pslot * SLOT;
 #pragma unroll
     for (int i = 0; i < PER; ++i)
       dma16(i < MT * 2 ? rx : rl, real ? off[i] + k : OOB, sl + i * 1024);
-    slot_p = slot_p + 1 == STAGES ? 0 : slot_p + 1;
-    ++ps;
-    // on to the next adapter without a gap, where no other wave takes part
-    if (apart && ps >= steps && pq < n) {
-      pq += qs;
-      ps = 0;
-      aim();
-    }
+    pslot = pslot + 1 == STAGES ? 0 : pslot + 1;
+    pk += WAVES;
+    if (pk >= nkb) aim();
   };
   const int lo = fr * 128 + ((fg ^ row_key(fr)) << 4), hi = fr * 128 + (((fg + 4) ^ row_key(fr)) << 4);
+  v4f acc[RT][MT];
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
+  aim();
+#pragma unroll
+  for (int s = 0; s < STAGES - 1; ++s) produce();
   int slot = 0;
-  for (int q = q0; q < n; q += qs) {
-    if (!apart || q == q0) {
-      pq = q;
-      ps = 0;
-      slot_p = slot = 0;
-      aim();
+  for (int e = wave; e < n * nkb; e += WAVES) {
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // the last block's fragments are in registers: its slot is free
+    asm volatile("" ::: "memory");
+    produce();
+    __builtin_amdgcn_s_waitcnt(vmcnt_imm(PER * (STAGES - 1)));  // this block has landed
+    asm volatile("" ::: "memory");
+    const uint8_t *sl = ring[wave] + slot * SLOT;
+    slot = slot + 1 == STAGES ? 0 : slot + 1;
+    bf16x8 a[MT][2], b[RT][2];
+    bf16_peak peak;
 #pragma unroll
-      for (int s = 0; s < STAGES - 1; ++s) produce();
+    for (int j = 0; j < MT; ++j) {
+      a[j][0] = *reinterpret_cast<const bf16x8 *>(sl + j * 2048 + lo);
+      a[j][1] = *reinterpret_cast<const bf16x8 *>(sl + j * 2048 + hi);
     }
-    v4f acc[RT][MT];
 #pragma unroll
-    for (int i = 0; i < RT; ++i)
-#pragma unroll
-      for (int j = 0; j < MT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-    for (int s = 0; s < steps; ++s) {
-      __builtin_amdgcn_s_waitcnt(0xC07F);  // the last block's fragments are in registers: its slot is free
-      asm volatile("" ::: "memory");
-      produce();
-      __builtin_amdgcn_s_waitcnt(vmcnt_imm(PER * (STAGES - 1)));  // this block has landed
-      asm volatile("" ::: "memory");
-      const uint8_t *sl = ring[wave] + slot * SLOT;
-      bf16x8 a[MT][2], b[RT][2];
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        a[j][0] = *reinterpret_cast<const bf16x8 *>(sl + j * 2048 + lo);
-        a[j][1] = *reinterpret_cast<const bf16x8 *>(sl + j * 2048 + hi);
-      }
-#pragma unroll
-      for (int i = 0; i < RT; ++i) {
-        b[i][0] = *reinterpret_cast<const bf16x8 *>(sl + (MT + i) * 2048 + lo);
-        b[i][1] = *reinterpret_cast<const bf16x8 *>(sl + (MT + i) * 2048 + hi);
-      }
+    for (int i = 0; i < RT; ++i) {
+      b[i][0] = *reinterpret_cast<const bf16x8 *>(sl + (MT + i) * 2048 + lo);
+      b[i][1] = *reinterpret_cast<const bf16x8 *>(sl + (MT + i) * 2048 + hi);
+      peak.see(__builtin_bit_cast(u32x4, b[i][0]));
+      peak.see(__builtin_bit_cast(u32x4, b[i][1]));
+    }
+    if (__ballot(!peak.finite()) == 0) {
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -199,63 +200,72 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
 #pragma unroll
           for (int j = 0; j < MT; ++j)
             acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i][h], a[j][h], acc[i][j], 0, 0, 0);
-      asm volatile("" ::: "memory");
-      slot = slot + 1 == STAGES ? 0 : slot + 1;
-    }
-    const int ad = s_list[q];
-    auto put = [&](const v4f &s, int i, int j) {  // ranks 4 fg .. 4 fg + 3 of the i-th 16, row fr of the j-th
-      const int r = r0 + i * 16 + 4 * fg, m = j * 16 + fr;
-      if (s_id[m] != ad || r >= R) return;  // R is a multiple of 8
-      const size_t at = (size_t)(m0 + m) * R + r;
-      if (gridDim.z > 1) {
-        *reinterpret_cast<v4f *>(planes + (size_t)blockIdx.z * M * R + at) = s;
-      } else {
-        const float f = scale[ad];
-        *reinterpret_cast<u32x2 *>(H + at) = u32x2{bf16_pair(f * s[0], f * s[1]), bf16_pair(f * s[2], f * s[3])};
-      }
-    };
-    if (apart) {
-#pragma unroll
-      for (int i = 0; i < RT; ++i)
-#pragma unroll
-        for (int j = 0; j < MT; ++j) put(acc[i][j], i, j);
     } else {
-      __builtin_amdgcn_s_waitcnt(0);  // nothing still lands in the ring, which the partial tiles reuse
-      v4f *part = reinterpret_cast<v4f *>(ring[wave]);
+      const int ad = s_list[e / nkb];
 #pragma unroll
-      for (int i = 0; i < RT; ++i)
+      for (int j = 0; j < MT; ++j) {
+        const bool mine = s_id[j * 16 + fr] == ad;
 #pragma unroll
-        for (int j = 0; j < MT; ++j) part[(i * MT + j) * 64 + lane] = acc[i][j];
-      __syncthreads();
+        for (int i = 0; i < RT; ++i) {
+          v4f p = {0.f, 0.f, 0.f, 0.f};
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i][0], a[j][0], p, 0, 0, 0);
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i][1], a[j][1], p, 0, 0, 0);
 #pragma unroll
-      for (int e = 0; e < RT * MT / WAVES; ++e) {
-        const int p = wave * (RT * MT / WAVES) + e;
-        v4f s = reinterpret_cast<const v4f *>(ring[0])[p * 64 + lane];
-#pragma unroll
-        for (int v = 1; v < WAVES; ++v) s += reinterpret_cast<const v4f *>(ring[v])[p * 64 + lane];
-        put(s, p / MT, p % MT);
+          for (int r = 0; r < 4; ++r) acc[i][j][r] += mine ? p[r] : 0.f;
+        }
       }
-      __syncthreads();  // all partial tiles read before the rings fill again
+    }
+    asm volatile("" ::: "memory");
+  }
+  __builtin_amdgcn_s_waitcnt(0);  // nothing still lands in the ring, which the partial tiles reuse
+  v4f *part = reinterpret_cast<v4f *>(ring[wave]);
+#pragma unroll
+  for (int i = 0; i < RT; ++i)
+#pragma unroll
+    for (int j = 0; j < MT; ++j) part[(i * MT + j) * 64 + lane] = acc[i][j];
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < RT * MT / WAVES; ++e) {
+    const int p = wave * (RT * MT / WAVES) + e;
+    v4f s = reinterpret_cast<const v4f *>(ring[0])[p * 64 + lane];
+#pragma unroll
+    for (int v = 1; v < WAVES; ++v) s += reinterpret_cast<const v4f *>(ring[v])[p * 64 + lane];
+    // ranks 4 fg .. 4 fg + 3 of the i-th 16, row fr of the j-th
+    const int i = p / MT, m = p % MT * 16 + fr, r = r0 + i * 16 + 4 * fg, ad = s_id[m];
+    if (ad < 0 || r >= R) continue;  // R is a multiple of 8
+    const size_t at = (size_t)(m0 + m) * R + r;
+    if (gridDim.z > 1) {
+      *reinterpret_cast<v4f *>(planes + (size_t)blockIdx.z * M * R + at) = s;
+    } else {
+      const float f = scale[ad];
+      *reinterpret_cast<u32x2 *>(H + at) = u32x2{bf16_pair(f * s[0], f * s[1]), bf16_pair(f * s[2], f * s[3])};
     }
   }
-  __builtin_amdgcn_s_waitcnt(0);  // nothing may still write LDS when the workgroup ends
 }
 
-// H from the partial planes, summed in order
+// H from the partial planes, summed in order; JOIN planes' loads at a time (those
+// past the last read zeros)
+constexpr int JOIN = 16;
 __global__ __launch_bounds__(256) void lora_join_kernel(const float *planes, const int32_t *ids,
                                                         const float *scale, uint16_t *H, int M, int R, int G,
                                                         int n) {
-  const long long q = (long long)blockIdx.x * 256 + threadIdx.x;
-  const int m = (int)(q / (R / 4));
+  const uint32_t q = blockIdx.x * 256 + threadIdx.x;
+  const int m = (int)(q / (uint32_t)(R / 4));
   if (m >= M) return;
   const int ad = ids[m];
   if (ad < 0 || ad >= G) return;
-  const size_t plane = (size_t)M * R;
-  v4f s = *reinterpret_cast<const v4f *>(planes + q * 4);
-#pragma unroll 4
-  for (int i = 1; i < n; ++i) s += *reinterpret_cast<const v4f *>(planes + i * plane + q * 4);
+  const uint32_t plane = (uint32_t)M * R * 4;
+  const __amdgpu_buffer_rsrc_t r = rsrc(planes, plane * n);
+  v4f s = {0.f, 0.f, 0.f, 0.f};
+  for (int i0 = 0; i0 < n; i0 += JOIN) {
+    u32x4 p[JOIN];
+#pragma unroll
+    for (int i = 0; i < JOIN; ++i) p[i] = load16(r, i0 + i < n ? q * 16 + (i0 + i) * plane : OOB);
+#pragma unroll
+    for (int i = 0; i < JOIN; ++i) s += __builtin_bit_cast(v4f, p[i]);
+  }
   const float f = scale[ad];
-  *reinterpret_cast<u32x2 *>(H + q * 4) = u32x2{bf16_pair(f * s[0], f * s[1]), bf16_pair(f * s[2], f * s[3])};
+  *reinterpret_cast<u32x2 *>(H + (size_t)q * 4) = u32x2{bf16_pair(f * s[0], f * s[1]), bf16_pair(f * s[2], f * s[3])};
 }
 
 constexpr int LORA_DOT = 8192;  // rows x ranks up to which the dot form is used
@@ -273,6 +283,7 @@ ShrinkPlan shrink_plan(int M, int K, int R) {
   p.ry = (R + p.rt * 16 - 1) / (p.rt * 16);
   // K blocks shared out until 256 workgroups run, at least one block a wave
   const int nkb = K / 64;
+  // (so the planes hold at most 256 tiles of 64 x 64: 4 MB)
   const int want = (int)std::max(1LL, 256LL / ((long long)p.tiles * p.ry));
   p.planes = std::max(1, std::min(want, nkb / WAVES));
   p.kb_per = nkb > 0 ? (nkb + p.planes - 1) / p.planes : 0;

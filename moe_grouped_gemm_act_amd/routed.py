@@ -21,7 +21,7 @@ import os
 
 import torch
 
-from . import HEADER, _check, _codes, _dev, _p, _shape, _stream, load_library
+from . import HEADER, Fp8GemmError, _codes, _shape, fp8gemm_status_string, load_library
 
 ROUTED_HEADER = os.path.join(os.path.dirname(HEADER), "fp8gemm_routed.h")
 
@@ -58,6 +58,35 @@ def _load():
         lib.lora_workspace.argtypes, lib.lora_workspace.restype = [i32] * 3, ctypes.c_longlong
         _routed = lib
     return _routed
+
+
+# the current stream's handle without a Stream object around it (2 us a call less)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda i: torch.cuda.current_stream(i).cuda_stream)
+
+
+def _p(t):
+    return t.data_ptr()
+
+
+def _dev(*ts):
+    """The GPU that holds every tensor, as an index."""
+    dev = ts[0].get_device()
+    for t in ts:
+        if t.get_device() != dev or dev < 0:
+            raise ValueError("all tensors must be on the same GPU")
+        if not t.is_contiguous():
+            raise ValueError("tensors must be contiguous")
+    return dev
+
+
+def _stream(stream, dev):
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
+
+
+def _check(status):
+    if status != 0:
+        raise Fp8GemmError(status, fp8gemm_status_string(status))
 
 
 def _typed(t, dtype, name):
@@ -120,7 +149,7 @@ def moe_contiguous_rows(choices, G):
 def _workspace(lib, S, G, device, stream):
     n = lib.moe_sort_workspace(S, G)
     if n == 0:
-        return None, ctypes.c_void_p(0)
+        return None, None
     ws = torch.empty(n, dtype=torch.int32, device=device)
     if stream is not None:
         ws.record_stream(stream)  # freed on return; the caching allocator waits for that stream
@@ -134,15 +163,15 @@ def moe_sort_contiguous(ids, G, M=None, row=None, m_indices=None, counts=None, s
     counts [G] int32).  M (a multiple of 128) defaults to
     moe_contiguous_rows(T k, G), which holds any ids."""
     S = ids.numel()
-    dev = ids.device
+    at = ids.device
     lib = _load()
     if M is None:
         M = lib.moe_contiguous_rows(S, G)
-    row = _out(row, ids.shape, torch.int32, dev, "row")
-    m_indices = _out(m_indices, (M,), torch.int32, dev, "m_indices")
-    counts = _out(counts, (G,), torch.int32, dev, "counts")
-    _dev(_typed(ids, torch.int32, "ids"), row, m_indices, counts)
-    ws, wp = _workspace(lib, S, G, dev, stream)
+    row = _out(row, ids.shape, torch.int32, at, "row")
+    m_indices = _out(m_indices, (M,), torch.int32, at, "m_indices")
+    counts = _out(counts, (G,), torch.int32, at, "counts")
+    dev = _dev(_typed(ids, torch.int32, "ids"), row, m_indices, counts)
+    ws, wp = _workspace(lib, S, G, at, stream)
     _check(lib.moe_sort_contiguous(_p(ids), _p(row), _p(m_indices), _p(counts), wp, S, G, M,
                                    _stream(stream, dev)))
     return row, m_indices, counts
@@ -153,12 +182,12 @@ def moe_sort_masked(ids, G, M, row=None, masked_m=None, stream=None):
     each: ids [T,k] int32 -> (row [T,k] int32: g * M + the place among expert
     g's rows, -1 past its M rows; masked_m [G] int32)."""
     S = ids.numel()
-    dev = ids.device
+    at = ids.device
     lib = _load()
-    row = _out(row, ids.shape, torch.int32, dev, "row")
-    masked_m = _out(masked_m, (G,), torch.int32, dev, "masked_m")
-    _dev(_typed(ids, torch.int32, "ids"), row, masked_m)
-    ws, wp = _workspace(lib, S, G, dev, stream)
+    row = _out(row, ids.shape, torch.int32, at, "row")
+    masked_m = _out(masked_m, (G,), torch.int32, at, "masked_m")
+    dev = _dev(_typed(ids, torch.int32, "ids"), row, masked_m)
+    ws, wp = _workspace(lib, S, G, at, stream)
     _check(lib.moe_sort_masked(_p(ids), _p(row), _p(masked_m), wp, S, G, M, _stream(stream, dev)))
     return row, masked_m
 
@@ -221,7 +250,7 @@ def moe_combine(Y, row, w=None, out=None, stream=None):
         dev = _dev(_typed(Y, torch.bfloat16, "Y"), row, w, out)
     else:
         dev = _dev(_typed(Y, torch.bfloat16, "Y"), row, out)
-    _check(_load().moe_combine_bf16(_p(Y), _p(row), ctypes.c_void_p(0) if w is None else _p(w),
+    _check(_load().moe_combine_bf16(_p(Y), _p(row), None if w is None else _p(w),
                                     _p(out), T, H, k, M, _stream(stream, dev)))
     return out
 
