@@ -34,22 +34,29 @@ static __device__ __forceinline__ uint32_t lane_of(uint32_t x, int l) {
   return (uint32_t)__builtin_amdgcn_readlane((int)x, l);
 }
 
-// the greatest of the wave's values (uniform)
-static __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+// over each row of 16 lanes, in every lane of it
+static __device__ __forceinline__ uint32_t row_max(uint32_t x) {
   x = max(x, dpp<DPP_XOR1>(x));
   x = max(x, dpp<DPP_XOR2>(x));
   x = max(x, dpp<DPP_HALF_MIRROR>(x));
-  x = max(x, dpp<DPP_MIRROR>(x));
+  return max(x, dpp<DPP_MIRROR>(x));
+}
+static __device__ __forceinline__ float row_sum(float f) {
+  f += __uint_as_float(dpp<DPP_XOR1>(__float_as_uint(f)));
+  f += __uint_as_float(dpp<DPP_XOR2>(__float_as_uint(f)));
+  f += __uint_as_float(dpp<DPP_HALF_MIRROR>(__float_as_uint(f)));
+  return f + __uint_as_float(dpp<DPP_MIRROR>(__float_as_uint(f)));
+}
+
+// the greatest of the wave's values (uniform)
+static __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  x = row_max(x);
   return max(max(lane_of(x, 0), lane_of(x, 16)), max(lane_of(x, 32), lane_of(x, 48)));
 }
 
 // the wave's sum, in one fixed order (uniform)
 static __device__ __forceinline__ float wave_sum(float f) {
-  f += __uint_as_float(dpp<DPP_XOR1>(__float_as_uint(f)));
-  f += __uint_as_float(dpp<DPP_XOR2>(__float_as_uint(f)));
-  f += __uint_as_float(dpp<DPP_HALF_MIRROR>(__float_as_uint(f)));
-  f += __uint_as_float(dpp<DPP_MIRROR>(__float_as_uint(f)));
-  const uint32_t u = __float_as_uint(f);
+  const uint32_t u = __float_as_uint(row_sum(f));
   return (__uint_as_float(lane_of(u, 0)) + __uint_as_float(lane_of(u, 16))) +
          (__uint_as_float(lane_of(u, 32)) + __uint_as_float(lane_of(u, 48)));
 }

@@ -66,7 +66,8 @@ def logits_for(rng, T, E, bf16):
 
 @pytest.mark.parametrize("bf16", [False, True])
 @pytest.mark.parametrize("T,E,k", [(1, 1, 1), (1, 8, 8), (7, 64, 6), (9, 65, 3), (33, 128, 8), (5, 160, 6),
-                                   (8, 256, 8), (11, 384, 9), (8, 511, 1), (7, 1000, 64), (8, 1024, 10)])
+                                   (8, 256, 8), (11, 384, 9), (8, 511, 1), (7, 1000, 64), (8, 1024, 10),
+                                   (4096, 64, 6), (4099, 128, 8), (4102, 200, 16), (4097, 511, 3), (4099, 33, 5), (4100, 256, 17)])
 def test_topk(T, E, k, bf16):
     rng = np.random.default_rng(5000 + T * E + k)
     x = logits_for(rng, T, E, bf16)
