@@ -132,11 +132,12 @@ int moe_combine_backward_bf16(const void *dout, const void *Y, const int32_t *ro
  * padded with zeros), scale [G] (fp32).  Rows may come in any order; adapters
  * that no row names are not read.
  *
- * h is an fp32 sum, scaled and rounded once to bf16 (it is an operand of the
- * second factor's product); h Lb^T is added into the base product's fp32
+ * h is an fp32 sum, scaled and, except for few rows, rounded once to bf16 (it
+ * is then a matrix instruction's operand); h Lb^T is added into the base product's fp32
  * accumulators, and D is rounded once.  A value that is not finite in one row
  * of X or in one adapter reaches the rows that use it alone.
- * ws: lora_workspace(M, K, R) bytes of the caller's, 16-byte aligned, contents
+ * ws: lora_workspace(M, N, K, R, fp8) bytes of the caller's (fp8: whether the
+ * base product is FP8), 16-byte aligned, contents
  * arbitrary, free again when the call's work is done.
  * The FP8 form quantises nothing: A and sa are the base product's operands and
  * X [M,K] (bf16) is what the adapters read.
@@ -144,7 +145,7 @@ int moe_combine_backward_bf16(const void *dout, const void *Y, const int32_t *ro
  * R <= 4096, G <= 4096; M R, N R and G N R below 2^30 (La may be larger); X, La
  * and Lb 16-byte aligned, ids and scale 4-byte.  R, G or K of 0: the base call.
  */
-long long lora_workspace(int M, int K, int R);
+long long lora_workspace(int M, int N, int K, int R, int fp8);
 
 int gemm_bf16_nt_lora(const void *A, const void *B, const void *La, const void *Lb, const int32_t *ids,
                       const float *scale, void *D, void *ws, int M, int N, int K, int R, int G,

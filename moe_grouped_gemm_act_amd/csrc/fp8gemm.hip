@@ -59,6 +59,7 @@
 #include "e4m3.h"
 #include "fp8gemm.h"
 #include "lora.h"
+#include "lora_dot.h"
 
 namespace {
 
@@ -92,6 +93,12 @@ struct Args {
   const uint16_t *lh, *lb;
   const int32_t *lids;
   int lr, lg;
+  // few rows: the first factor's operands and result (fp32 [M][lr]), formed by
+  // the first `dots` workgroups of the launch
+  const uint16_t *lx, *lla;
+  const float *lscale;
+  float *lhf;
+  int dots;
 };
 
 // XOR key of an LDS row: 16-byte chunk c of row r sits at position
@@ -595,7 +602,13 @@ __device__ __forceinline__ void store_bf16(const v4f (&acc)[TN][TM], uint16_t *D
 // is an out-of-range load: zeros, no traffic.  So every adapter's rows are read
 // once a weight tile whatever the order of the requests, and a tile pays
 // ceil(adapters lr / 64) blocks beside its K / 64 (BF16) or K / 128 (FP8).
+//
+// LORA_BLOCKS is that.  LORA_DOTS (few rows): the launch holds, before the base
+// product's workgroups, others that form h by dot products at the same time;
+// the base product goes to fp32 planes, whatever its K split, and a second
+// kernel joins the planes and h Lb^T (lora.hip).
 constexpr int LORA_MAXG = 4096;
+constexpr int LORA_BLOCKS = 1, LORA_DOTS = 2;
 
 // One wave lists the distinct adapters of the tile's BM rows in ascending
 // order (a bitmap over all lg) while the loaders fetch the first blocks.
@@ -689,8 +702,9 @@ __device__ __forceinline__ void adapter_kblock(const uint8_t *sl, int e0, int R,
 }
 
 template <int WGN, int WGM, int TN, int TM, int STAGES, int NLD, bool KSPLIT, bool ACT, int LAYOUT,
-          bool BF = false, bool LORA = false>
+          bool BF = false, int ADAPT = 0>
 __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
+  constexpr bool LORA = ADAPT == LORA_BLOCKS;
   constexpr int BN = WGN * TN * 16, BM = WGM * TM * 16;
   constexpr int ROWS = BM + BN;
   // BF: bf16 operands with no scales; a "K block" is then 128 bytes = 64 elements
@@ -715,7 +729,7 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
   // 128 columns of y
   static_assert(!ACT || (BN == 256 && WGN == 4 && TN == 4 && BM <= 128), "SwiGLU tile shape");
   static_assert(!(ACT && BF), "the fused SwiGLU takes FP8 operands");
-  static_assert(!LORA || (LAYOUT == DENSE && !ACT && NLD % 2 == 0), "adapters: dense tiles");
+  static_assert(ADAPT == 0 || (LAYOUT == DENSE && !ACT && NLD % 2 == 0), "adapters: dense tiles");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[STAGES][SLOT];
   __shared__ float s_sb[BN > 128 || TWOB ? 2 : 1][BF ? 1 : MAXKB];
   __shared__ float s_rmax[ACT ? 4 * BM : 1];  // ACT: row maxima of y per wave column
@@ -736,12 +750,23 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
   // XCD share panels
   constexpr int GROUPN = 4;
   const int T = a.tiles_m * a.tiles_n, S = KSPLIT ? a.splits : 1;
+  if constexpr (ADAPT == LORA_DOTS) {
+    if ((int)blockIdx.x < a.dots) {  // one rank of one row per wave
+      const int q = (int)blockIdx.x * (NCW + NLD) + wave, m = q / a.lr;
+      if (m >= M) return;
+      const int ad = a.lids[m];
+      if (ad < 0 || ad >= a.lg) return;
+      const float h = lora_dot<8>(a.lx, a.lla, m, q % a.lr, ad, K, a.lr, lane);
+      if (lane == 0) a.lhf[q] = a.lscale[ad] * h;
+      return;
+    }
+  }
   // Tail split: when the last wave of tiles would leave most CUs idle, the
   // tiles past full_tiles are split over K.  Their items take the highest
   // workgroup ids, which are dispatched last, once CUs free up, round robin
   // over the XCDs; the full tiles keep the XCD-aware order below.
   const bool tail = !KSPLIT && LAYOUT == DENSE && a.tail_splits > 1 && (int)blockIdx.x >= a.full_tiles;
-  int item = blockIdx.x, split, tile;
+  int item = ADAPT == LORA_DOTS ? (int)blockIdx.x - a.dots : (int)blockIdx.x, split, tile;
   if (tail) {
     const int r = item - a.full_tiles;
     tile = a.full_tiles + r / a.tail_splits;
@@ -1011,7 +1036,7 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
                            wn, wm, fr, fg);
     return;
   }
-  if (S > 1) {
+  if (S > 1 || ADAPT == LORA_DOTS) {
     // this split's fp32 partial goes to its own [M][N] plane of the
     // workspace; splitk_reduce_kernel (next on the stream) sums the planes
 #pragma unroll
@@ -1688,7 +1713,7 @@ float *scratch_ptr() {
 }
 
 template <int WGN, int WGM, int TN, int TM, int STAGES, int NLD, int LAYOUT, bool KSPLIT = false,
-          bool ACT = false, bool BF = false, bool LORA = false>
+          bool ACT = false, bool BF = false, int ADAPT = 0>
 int launch_tile(Args a, int groups, hipStream_t stream) {
   a.tiles_m = cdiv(a.M, WGM * TM * 16);
   a.tiles_n = cdiv(a.N, WGN * TN * 16);
@@ -1696,11 +1721,13 @@ int launch_tile(Args a, int groups, hipStream_t stream) {
     a.splits = 1;
     a.kb_per_split = (BF ? 2 * a.K : a.K) / BK;
   }
+  if (ADAPT == LORA_DOTS)  // whole rounds of the 8 XCDs, so that the tiles behind keep theirs
+    a.dots = cdiv(cdiv(a.M * a.lr, WGN * WGM + NLD), 8) * 8;
   void *kargs[] = {&a};
   hipError_t e = hipLaunchKernel(
       reinterpret_cast<const void *>(
-          &tile_kernel<WGN, WGM, TN, TM, STAGES, NLD, KSPLIT, ACT, LAYOUT, BF, LORA>),
-      dim3(a.tiles_m * a.tiles_n * a.splits, groups), dim3((WGN * WGM + NLD) * 64), kargs, 0,
+          &tile_kernel<WGN, WGM, TN, TM, STAGES, NLD, KSPLIT, ACT, LAYOUT, BF, ADAPT>),
+      dim3(a.tiles_m * a.tiles_n * a.splits + a.dots, groups), dim3((WGN * WGM + NLD) * 64), kargs, 0,
       stream);
   return e == hipSuccess ? FP8GEMM_OK : FP8GEMM_LAUNCH_FAILED;
 }
@@ -1729,9 +1756,9 @@ bool decode_built(int bn, int stages, int bm, int waves) {
 // byte); a K split only when the tiles alone leave CUs idle, with (tiles x
 // splits) kept within one wave of 256 workgroups and at least 9 K blocks per
 // split, since the partial planes and their reduction cost about 3 us.
-DecodeCfg decode_config(int M, int N, int Kb, bool bf) {
+DecodeCfg decode_config(int M, int N, int Kb, bool bf, bool override = true) {
   const int bm = M <= 64 ? 64 : 128;
-  const char *e = getenv("FP8GEMM_DECODE");
+  const char *e = override ? getenv("FP8GEMM_DECODE") : nullptr;
   DecodeCfg o{0, 0, 0, 4};
   if (e && sscanf(e, "%d,%d,%d,%d", &o.bn, &o.stages, &o.splits, &o.waves) >= 3 && o.splits >= 1 &&
       decode_built(o.bn, o.stages, bm, o.waves))
@@ -1764,22 +1791,28 @@ DecodeCfg decode_config(int M, int N, int Kb, bool bf) {
   return c;
 }
 
+// the K split as run: no split without a block
+void decode_splits(const DecodeCfg &c, int Kb, int &splits, int &per) {
+  splits = std::max(1, std::min(c.splits, std::max(Kb, 1)));
+  per = Kb > 0 ? cdiv(Kb, splits) : 0;
+  splits = Kb > 0 ? cdiv(Kb, per) : 1;
+}
+
 // BF: bf16 operands, K blocks of 64 elements (128 bytes)
 // fixed_ws: a caller-provided scratch of SCRATCH_FLOATS (the allocation-free
 // entry point); nullptr: the library workspace (WsLease)
-// LORA: with the adapters' blocks (spread over the K splits)
-template <bool BF, bool LORA = false>
+// ADAPT: LORA_BLOCKS: with the adapters' blocks, spread over the K splits;
+// LORA_DOTS: a.ws is the caller's and takes a plane per split, for one split
+// too; the caller joins them
+template <bool BF, int ADAPT = 0>
 int run_decode(Args a, hipStream_t stream, float *fixed_ws = nullptr) {
   const int Kb = (BF ? 2 * a.K : a.K) / BK;
-  DecodeCfg c = decode_config(a.M, a.N, Kb, BF);
+  DecodeCfg c = decode_config(a.M, a.N, Kb, BF, ADAPT != LORA_DOTS);
   const int bm = a.M <= 64 ? 64 : 128;
-  int splits = std::max(1, std::min(c.splits, std::max(Kb, 1)));
-  const int kps = Kb > 0 ? cdiv(Kb, splits) : 0;
-  splits = Kb > 0 ? cdiv(Kb, kps) : 1;
-  a.splits = splits;
-  a.kb_per_split = kps;
+  decode_splits(c, Kb, a.splits, a.kb_per_split);
+  const int splits = a.splits;
   WsLease ws;  // held until the reduction is enqueued
-  if (splits > 1) {
+  if (splits > 1 && ADAPT != LORA_DOTS) {
     const size_t need = (size_t)splits * a.M * a.N;
     if (fixed_ws) {
       if (need > SCRATCH_FLOATS) return FP8GEMM_SCRATCH_EXCEEDED;
@@ -1794,22 +1827,24 @@ int run_decode(Args a, hipStream_t stream, float *fixed_ws = nullptr) {
   int st = FP8GEMM_LAUNCH_FAILED;  // unreachable: decode_config returns built instances only
   if (c.waves == 8) {
     if (c.bn == 128)
-      st = bm == 64 ? launch_tile<2, 4, 4, 1, 4, 4, DENSE, true, false, BF, LORA>(a, 1, stream)
-                    : launch_tile<2, 4, 4, 2, 4, 4, DENSE, true, false, BF, LORA>(a, 1, stream);
+      st = bm == 64 ? launch_tile<2, 4, 4, 1, 4, 4, DENSE, true, false, BF, ADAPT>(a, 1, stream)
+                    : launch_tile<2, 4, 4, 2, 4, 4, DENSE, true, false, BF, ADAPT>(a, 1, stream);
     else
-      st = launch_tile<2, 4, 2, 2, 4, 4, DENSE, true, false, BF, LORA>(a, 1, stream);
+      st = launch_tile<2, 4, 2, 2, 4, 4, DENSE, true, false, BF, ADAPT>(a, 1, stream);
   }
 #define DEC(BN_, ST_)                                                                     \
   if (c.waves == 4 && c.bn == BN_ && c.stages == ST_)                                     \
-    st = bm == 64 ? launch_tile<1, 4, BN_ / 16, 1, ST_, 4, DENSE, true, false, BF, LORA>(a, 1, stream) \
-                  : launch_tile<1, 4, BN_ / 16, 2, ST_, 4, DENSE, true, false, BF, LORA>(a, 1, stream);
+    st = bm == 64 ? launch_tile<1, 4, BN_ / 16, 1, ST_, 4, DENSE, true, false, BF, ADAPT>(a, 1, stream) \
+                  : launch_tile<1, 4, BN_ / 16, 2, ST_, 4, DENSE, true, false, BF, ADAPT>(a, 1, stream);
   DEC(64, 4)
-  DEC(64, 6)
+  if constexpr (ADAPT != LORA_DOTS) {  // reached through the override alone
+    DEC(64, 6)
+  }
   DEC(128, 4)
   DEC(96, 4)
   DEC(32, 4)
 #undef DEC
-  if (st != FP8GEMM_OK || a.splits == 1) return st;
+  if (st != FP8GEMM_OK || a.splits == 1 || ADAPT == LORA_DOTS) return st;
   const long long quads = (long long)a.M * cdiv(a.N, 4);
   const dim3 grid((unsigned)((quads + 255) / 256));
   // the launch's own status (hipGetLastError would also report an earlier
@@ -1884,8 +1919,8 @@ hipError_t launch_walk(Args &a, int P, hipStream_t stream) {
 // S = min(8, 256 / R) parts (each at least 4 K blocks) that run as the last
 // items of the same grid, and tail_reduce_kernel adds the parts.  Without a
 // workspace the tail is not split.
-// LORA: one workgroup per tile (the walk has no adapter blocks).
-template <int WGN, int WGM, int TN, int TM, int STAGES, int NLD, bool BF = false, bool LORA = false>
+// ADAPT: one workgroup per tile (the walk has no adapter blocks).
+template <int WGN, int WGM, int TN, int TM, int STAGES, int NLD, bool BF = false, int ADAPT = 0>
 int launch_dense_large(Args a, hipStream_t stream, float *fixed_ws = nullptr) {
   constexpr int BN = WGN * TN * 16, BM = WGM * TM * 16;
   const int tiles_m = cdiv(a.M, BM), tiles_n = cdiv(a.N, BN), T = tiles_m * tiles_n;
@@ -1903,13 +1938,13 @@ int launch_dense_large(Args a, hipStream_t stream, float *fixed_ws = nullptr) {
   }
   // more tiles than CUs: the persistent walk over the same items
   const int P = walk_workgroups();
-  const bool walk = !LORA && walk_enabled(BF ? 2 * a.K : a.K) && P >= 8 && T > P;
+  const bool walk = ADAPT == 0 && walk_enabled(BF ? 2 * a.K : a.K) && P >= 8 && T > P;
   a.tiles_m = tiles_m;
   a.tiles_n = tiles_n;
   a.splits = 1;
   a.kb_per_split = Kb;
   if (S <= 1) {
-    if (!walk) return launch_tile<WGN, WGM, TN, TM, STAGES, NLD, DENSE, false, false, BF, LORA>(a, 1, stream);
+    if (!walk) return launch_tile<WGN, WGM, TN, TM, STAGES, NLD, DENSE, false, false, BF, ADAPT>(a, 1, stream);
     return launch_walk<WGN, WGM, TN, TM, STAGES, NLD, DENSE, BF>(a, P, stream) == hipSuccess
                ? FP8GEMM_OK
                : FP8GEMM_LAUNCH_FAILED;
@@ -1926,7 +1961,7 @@ int launch_dense_large(Args a, hipStream_t stream, float *fixed_ws = nullptr) {
     void *kargs[] = {&a};
     er = hipLaunchKernel(
         reinterpret_cast<const void *>(
-            &tile_kernel<WGN, WGM, TN, TM, STAGES, NLD, false, false, DENSE, BF, LORA>),
+            &tile_kernel<WGN, WGM, TN, TM, STAGES, NLD, false, false, DENSE, BF, ADAPT>),
         dim3(a.full_tiles + R * a.tail_splits), dim3((WGN * WGM + NLD) * 64), kargs, 0, stream);
   }
   if (er != hipSuccess) return FP8GEMM_LAUNCH_FAILED;
@@ -2233,17 +2268,42 @@ int lora_product_check(const LoraProduct &p) {
   return FP8GEMM_OK;
 }
 
-int lora_product(const LoraProduct &p) {
+static Args lora_args(const LoraProduct &p) {
   Args a{static_cast<const uint8_t *>(p.A), p.sa, static_cast<const uint8_t *>(p.B), p.sb,
          static_cast<uint16_t *>(p.D), p.M, p.N, p.K, 1, nullptr, 0, 0, 1,
          (p.fp8 ? p.K : 2 * p.K) / BK, nullptr};
-  a.lh = static_cast<const uint16_t *>(p.H);
-  a.lb = static_cast<const uint16_t *>(p.Lb);
   a.lids = p.ids;
   a.lr = p.R;
   a.lg = p.G;
+  return a;
+}
+
+int lora_product(const LoraProduct &p) {
+  Args a = lora_args(p);
+  a.lh = static_cast<const uint16_t *>(p.H);
+  a.lb = static_cast<const uint16_t *>(p.Lb);
   hipStream_t s = static_cast<hipStream_t>(p.stream);
+  constexpr int ADAPT = LORA_BLOCKS;
   if (p.fp8)
-    return p.M <= 128 ? run_decode<false, true>(a, s) : launch_dense_large<4, 2, 4, 4, 3, 4, false, true>(a, s);
-  return p.M <= 128 ? run_decode<true, true>(a, s) : launch_dense_large<2, 4, 4, 4, 3, 4, true, true>(a, s);
+    return p.M <= 128 ? run_decode<false, ADAPT>(a, s) : launch_dense_large<4, 2, 4, 4, 3, 4, false, ADAPT>(a, s);
+  return p.M <= 128 ? run_decode<true, ADAPT>(a, s) : launch_dense_large<2, 4, 4, 4, 3, 4, true, ADAPT>(a, s);
+}
+
+int lora_base_planes(int M, int N, int K, bool fp8) {
+  const int Kb = (fp8 ? K : 2 * K) / BK;
+  int splits, per;
+  decode_splits(decode_config(M, N, Kb, !fp8, false), Kb, splits, per);
+  return splits;
+}
+
+int lora_base_and_dots(const LoraProduct &p, const void *X, const void *La, const float *scale, float *h,
+                       float *planes) {
+  Args a = lora_args(p);
+  a.ws = planes;
+  a.lx = static_cast<const uint16_t *>(X);
+  a.lla = static_cast<const uint16_t *>(La);
+  a.lscale = scale;
+  a.lhf = h;
+  hipStream_t s = static_cast<hipStream_t>(p.stream);
+  return p.fp8 ? run_decode<false, LORA_DOTS>(a, s) : run_decode<true, LORA_DOTS>(a, s);
 }

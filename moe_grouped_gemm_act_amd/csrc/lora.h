@@ -20,3 +20,9 @@ struct LoraProduct {
 int lora_product_check(const LoraProduct &p);
 // after a check that gave FP8GEMM_OK
 int lora_product(const LoraProduct &p);
+// Few rows (M <= 128): the base product's fp32 planes [n][M][N], n =
+// lora_base_planes(...), and h [M][R] (fp32, scaled; rows without an adapter
+// are not written) in one launch; p.H is not used.
+int lora_base_planes(int M, int N, int K, bool fp8);
+int lora_base_and_dots(const LoraProduct &p, const void *X, const void *La, const float *scale, float *h,
+                       float *planes);

@@ -5,11 +5,15 @@
 // rounded to bf16 because it is a matrix instruction's operand there; the sums
 // before and after are fp32.
 //
-// Bound by reading X and the adapters in use once.  Two forms:
-//   * few rows (decode, M R <= LORA_DOT): one wave per row and rank, a dot
-//     product along K with all of its 16-byte loads in flight at once.  Every
-//     row reads its adapter's factor itself, which costs nothing when the rows
-//     name different adapters and little while they are few.
+// Bound by reading X and the adapters in use once.  Three forms:
+//   * few rows (decode, M R N <= LORA_FEW): one wave per row and rank, a dot
+//     product along K with all of its 16-byte loads in flight at once, in the
+//     base product's own launch; the base product's fp32 planes and h Lb^T are
+//     joined by a second launch, so a decode product is two launches and H
+//     stays fp32.  Every row reads its adapter's factors itself, which costs
+//     nothing when the rows name different adapters and little while they are
+//     few.
+//   * M R <= LORA_DOT: the same dot products in a launch of their own.
 //   * more rows: 64 rows x RT 16 ranks a workgroup on the matrix cores, K
 //     split over workgroups until they fill the chip; the fp32 partial planes
 //     are summed in order by a second, small kernel.
@@ -22,6 +26,7 @@
 #include "bf16.h"
 #include "fp8gemm_routed.h"
 #include "lora.h"
+#include "lora_dot.h"
 
 namespace {
 
@@ -42,8 +47,6 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, uint32_t off, vo
 constexpr int vmcnt_imm(int n) { return (n & 15) | (((n >> 4) & 3) << 14) | 0x0F70; }
 
 // ---- few rows ----------------------------------------------------------------
-// Wave r of the grid's row m: U 16-byte pieces of X's row and of the adapter's
-// row a time (512 elements each over the wave); pieces past K read zeros.
 constexpr int DOT_WAVES = 4;
 
 template <int U>
@@ -54,26 +57,81 @@ __global__ __launch_bounds__(DOT_WAVES * 64) void lora_dot_kernel(const uint16_t
   const int m = blockIdx.y, r = blockIdx.x * DOT_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int ad = ids[m];
   if (r >= R || ad < 0 || ad >= G) return;
-  const __amdgpu_buffer_rsrc_t rx = rsrc(X + (size_t)m * K, (uint32_t)K * 2);
-  const __amdgpu_buffer_rsrc_t rl = rsrc(La + ((size_t)ad * R + r) * K, (uint32_t)K * 2);
-  float acc[2] = {0.f, 0.f};
-  for (uint32_t k = lane * 16; k < (uint32_t)K * 2 + lane * 16; k += U * 1024) {
-    u32x4 x[U], l[U];
+  const float s = lora_dot<U>(X, La, m, r, ad, K, R, lane);
+  if (lane == 0) H[(size_t)m * R + r] = (uint16_t)bf16_of(scale[ad] * s);
+}
+
+// D[m][n] = bf16(sum of the base product's planes, in order, + h[m] . Lb[a][n]).
+// A wave takes B x 64 columns of one row.  P lanes (a power of two) share a
+// column's ranks, 8 (16 bytes) a lane and turn, so a load instruction reads
+// 1 KB of Lb in a row; the column's sum then goes to one lane of the P, chosen
+// so that the 64 lanes end with the 64 columns of a batch.
+template <int P, int B>
+__global__ __launch_bounds__(256) void lora_expand_kernel(const float *planes, int n_planes, const float *h,
+                                                          const uint16_t *Lb, const int32_t *ids,
+                                                          uint16_t *D, int M, int N, int R, int G) {
+  const int lane = threadIdx.x & 63, p = lane % P, g = lane / P;
+  constexpr int COLS = 64 / P;  // columns of one load instruction
+  const int m = blockIdx.y, n0 = (blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * B * 64;
+  if (n0 >= N) return;
+  const int ad = ids[m];
+  float v[B];  // column n0 + b 64 + p COLS + g
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      x[u] = load16(rx, k + u * 1024);
-      l[u] = load16(rl, k + u * 1024);
+  for (int b = 0; b < B; ++b) v[b] = 0.f;
+  if (ad >= 0 && ad < G) {
+    const __amdgpu_buffer_rsrc_t rl = rsrc(Lb + (size_t)ad * N * R, (uint32_t)N * R * 2);  // columns past N: zeros
+    const __amdgpu_buffer_rsrc_t rh = rsrc(h + (size_t)m * R, (uint32_t)R * 4);
+    for (int r0 = 0; r0 < R; r0 += P * 8) {
+      const int r = r0 + p * 8;
+      const bool live = r < R;
+      u32x4 l[B][P];
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int u = 0; u < P; ++u) {
+          const int n = n0 + b * 64 + u * COLS + g;
+          l[b][u] = load16(rl, live && n < N ? ((uint32_t)n * R + r) * 2 : OOB);
+        }
+      const v4f h0 = __builtin_bit_cast(v4f, load16(rh, live ? r * 4 : OOB));
+      const v4f h1 = __builtin_bit_cast(v4f, load16(rh, live ? r * 4 + 16 : OOB));
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int u = 0; u < P; ++u) {
+          const u32x4 w = l[b][u];
+          float s = h0[0] * bf16_lo(w[0]);
+          s = __builtin_fmaf(h0[1], bf16_hi(w[0]), s);
+          s = __builtin_fmaf(h0[2], bf16_lo(w[1]), s);
+          s = __builtin_fmaf(h0[3], bf16_hi(w[1]), s);
+          s = __builtin_fmaf(h1[0], bf16_lo(w[2]), s);
+          s = __builtin_fmaf(h1[1], bf16_hi(w[2]), s);
+          s = __builtin_fmaf(h1[2], bf16_lo(w[3]), s);
+          s = __builtin_fmaf(h1[3], bf16_hi(w[3]), s);
+          if (P > 1) s += __uint_as_float(dpp<DPP_XOR1>(__float_as_uint(s)));
+          if (P > 2) s += __uint_as_float(dpp<DPP_XOR2>(__float_as_uint(s)));
+          if (P > 4) s += __uint_as_float(dpp<DPP_HALF_MIRROR>(__float_as_uint(s)));
+          if (p == u) v[b] += s;
+        }
+    }
+  }
+  const size_t plane = (size_t)M * N;
+  float d[B];
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    const int n = n0 + b * 64 + p * COLS + g;
+    d[b] = n < N ? planes[(size_t)m * N + n] : 0.f;
+  }
+  for (int i = 1; i < n_planes; ++i)
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int n = n0 + b * 64 + p * COLS + g;
+      if (n < N) d[b] += planes[i * plane + (size_t)m * N + n];
     }
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        acc[0] = __builtin_fmaf(bf16_lo(x[u][e]), bf16_lo(l[u][e]), acc[0]);
-        acc[1] = __builtin_fmaf(bf16_hi(x[u][e]), bf16_hi(l[u][e]), acc[1]);
-      }
+  for (int b = 0; b < B; ++b) {
+    const int n = n0 + b * 64 + p * COLS + g;
+    if (n < N) D[(size_t)m * N + n] = (uint16_t)bf16_of(d[b] + v[b]);
   }
-  const float s = wave_sum(acc[0] + acc[1]);
-  if (lane == 0) H[(size_t)m * R + r] = (uint16_t)bf16_of(scale[ad] * s);
 }
 
 // ---- more rows ---------------------------------------------------------------
@@ -268,7 +326,18 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const float *planes, con
   *reinterpret_cast<u32x2 *>(H + (size_t)q * 4) = u32x2{bf16_pair(f * s[0], f * s[1]), bf16_pair(f * s[2], f * s[3])};
 }
 
-constexpr int LORA_DOT = 8192;  // rows x ranks up to which the dot form is used
+// Rows x ranks up to which h comes from dot products, and rows x ranks x columns
+// up to which that happens in the base product's launch, with the second factor
+// in the join, for M <= 128.  Whole calls there and as K blocks, in us, the rows
+// all of different adapters | all of one: 1 x 4096 x 7168 BF16 rank 64 15.5 and
+// 20.7; 64 x 7168 x 2048 FP8 rank 64 (2^24.8) 18.6 and 34.2 | 14.6 and 15.3;
+// 128 x 24576 x 1536 FP8 rank 16 (2^25.6) 32.4 and 26.8 | 23.6 and 16.4.
+constexpr int LORA_DOT = 8192;
+constexpr long long LORA_FEW = 1LL << 25;
+
+bool few_rows(int M, int N, int R) {
+  return M <= 128 && (long long)M * R <= LORA_DOT && (long long)M * R * N <= LORA_FEW;
+}
 
 struct ShrinkPlan {
   bool dot;
@@ -323,6 +392,26 @@ int shrink(const void *X, const void *La, const int32_t *ids, const float *scale
 
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) % n) == 0; }
 
+int product_few(const LoraProduct &p, const void *X, const void *La, const float *scale, void *ws) {
+  float *h = static_cast<float *>(ws);
+  float *planes = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + h_bytes(p.M, p.R) * 2);
+  const int st = lora_base_and_dots(p, X, La, scale, h, planes);
+  if (st != FP8GEMM_OK) return st;
+  LoraProduct q = p;
+  int n = lora_base_planes(p.M, p.N, p.K, p.fp8);
+  void *args[] = {&planes, &n, &h, &q.Lb, &q.ids, &q.D, &q.M, &q.N, &q.R, &q.G};
+  // 64 columns a wave until that makes more waves than the chip holds at once
+  const bool wide = (long long)p.M * p.N > 64LL * 8192;
+  const void *f = p.R <= 8    ? (wide ? reinterpret_cast<const void *>(&lora_expand_kernel<1, 4>)
+                                      : reinterpret_cast<const void *>(&lora_expand_kernel<1, 1>))
+                  : p.R <= 16 ? (wide ? reinterpret_cast<const void *>(&lora_expand_kernel<2, 4>)
+                                      : reinterpret_cast<const void *>(&lora_expand_kernel<2, 1>))
+                  : p.R <= 32 ? reinterpret_cast<const void *>(&lora_expand_kernel<4, 1>)
+                              : reinterpret_cast<const void *>(&lora_expand_kernel<8, 1>);
+  const int cols = wide && p.R <= 16 ? 1024 : 256;
+  return launch(f, dim3((p.N + cols - 1) / cols, p.M), 256, args, p.stream);
+}
+
 // every check, then the first factor's product and the whole
 int product(LoraProduct p, const void *X, const void *La, const float *scale, void *ws) {
   p.H = ws;
@@ -333,6 +422,7 @@ int product(LoraProduct p, const void *X, const void *La, const float *scale, vo
   if (!X || !La || !scale) return FP8GEMM_INVALID_ARG;
   if (p.K >= 1 << 23) return FP8GEMM_UNSUPPORTED_SHAPE;
   if (!aligned(X, 16) || !aligned(La, 16) || !aligned(scale, 4)) return FP8GEMM_MISALIGNED;
+  if (few_rows(p.M, p.N, p.R)) return product_few(p, X, La, scale, ws);
   float *planes = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + h_bytes(p.M, p.R));
   const int s2 = shrink(X, La, p.ids, scale, ws, planes, p.M, p.K, p.R, p.G, p.stream);
   return s2 != FP8GEMM_OK ? s2 : lora_product(p);
@@ -342,8 +432,10 @@ int product(LoraProduct p, const void *X, const void *La, const float *scale, vo
 
 extern "C" {
 
-long long lora_workspace(int M, int K, int R) {
-  if (M <= 0 || K <= 0 || R <= 0) return 0;
+long long lora_workspace(int M, int N, int K, int R, int fp8) {
+  if (M <= 0 || N <= 0 || K <= 0 || R <= 0) return 0;
+  if (few_rows(M, N, R))
+    return (long long)(h_bytes(M, R) * 2 + (size_t)lora_base_planes(M, N, K, fp8 != 0) * M * N * 4);
   const ShrinkPlan p = shrink_plan(M, K, R);
   return (long long)(h_bytes(M, R) + (p.dot || p.planes == 1 ? 0 : (size_t)p.planes * M * R * 4));
 }

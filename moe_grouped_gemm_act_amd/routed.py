@@ -21,7 +21,7 @@ import os
 
 import torch
 
-from . import HEADER, Fp8GemmError, _codes, _shape, fp8gemm_status_string, load_library
+from . import HEADER, Fp8GemmError, _codes, fp8gemm_status_string, load_library
 
 ROUTED_HEADER = os.path.join(os.path.dirname(HEADER), "fp8gemm_routed.h")
 
@@ -55,7 +55,7 @@ def _load():
                 ("gemm_fp8_1x128_128x128_bf16_lora", [vp] * 11 + [i32] * 5 + [vp])):
             f = getattr(lib, name)
             f.argtypes, f.restype = args, i32
-        lib.lora_workspace.argtypes, lib.lora_workspace.restype = [i32] * 3, ctypes.c_longlong
+        lib.lora_workspace.argtypes, lib.lora_workspace.restype = [i32] * 5, ctypes.c_longlong
         _routed = lib
     return _routed
 
@@ -67,6 +67,11 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
 
 def _p(t):
     return t.data_ptr()
+
+
+def _shape(t, shape, name):
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
 def _dev(*ts):
@@ -286,8 +291,8 @@ def _adapters(base, X, M, K, N, La, Lb, ids, scale, D, stream):
     _shape(_typed(Lb, torch.bfloat16, "Lb"), (G, N, R), "Lb")
     _shape(_typed(ids, torch.int32, "ids"), (M,), "ids")
     _shape(_typed(scale, torch.float32, "scale"), (G,), "scale")
-    dev = _dev(*base, X, La, Lb, ids, scale, D)
-    ws = torch.empty(_load().lora_workspace(M, K, R), dtype=torch.uint8, device=D.device)
+    dev = _dev(*base, La, Lb, ids, scale, D)
+    ws = torch.empty(_load().lora_workspace(M, N, K, R, len(base) == 5), dtype=torch.uint8, device=D.device)
     if stream is not None:
         ws.record_stream(stream)  # freed on return; the caching allocator waits for that stream
     return R, G, dev, ws
@@ -319,7 +324,7 @@ def gemm_fp8_1x128_128x128_bf16_lora(A, sa, B, sb, X, La, Lb, ids, scale, D=None
     _shape(_typed(sa, torch.float32, "sa"), (K // 128, M), "sa")
     _shape(_typed(sb, torch.float32, "sb"), ((N + 127) // 128, K // 128), "sb")
     D = _out(D, (M, N), torch.bfloat16, A.device, "D")
-    R, G, dev, ws = _adapters((A, sa, B, sb), X, M, K, N, La, Lb, ids, scale, D, stream)
+    R, G, dev, ws = _adapters((A, sa, B, sb, X), X, M, K, N, La, Lb, ids, scale, D, stream)
     _check(_load().gemm_fp8_1x128_128x128_bf16_lora(
         _p(A), _p(sa), _p(B), _p(sb), _p(X), _p(La), _p(Lb), _p(ids), _p(scale), _p(D), _p(ws),
         M, N, K, R, G, _stream(stream, dev)))

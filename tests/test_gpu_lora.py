@@ -105,6 +105,7 @@ SHAPES = [  # M, N, K, R, G
     (64, 4096, 2048, 16, 64), (64, 24576, 256, 8, 5), (65, 1000, 640, 72, 9), (128, 4096, 1024, 32, 128),
     (128, 24600, 128, 16, 33), (129, 257, 256, 16, 7), (300, 1030, 512, 40, 3), (515, 2112, 384, 128, 12),
     (200, 150, 960, 64, 3), (257, 300, 7168, 48, 2), (600, 70, 2048, 16, 300), (150, 64, 1024, 200, 5),
+    (16, 300, 512, 128, 5), (2, 4099, 256, 1024, 3), (30, 1000, 128, 64, 7), (9, 500, 256, 40, 4), (33, 2112, 640, 32, 33),
     (1100, 3700, 256, 64, 4096),
 ]
 
@@ -137,10 +138,10 @@ def test_few_base_blocks(K, fp8):
 
 
 @pytest.mark.parametrize("fp8", [False, True])
-@pytest.mark.parametrize("M,N", [(40, 320), (64, 4096), (300, 520)])
-def test_an_adapter_with_nan_and_inf_reaches_its_own_rows_alone(M, N, fp8):
-    announce(f"lora wild adapter M={M} N={N} fp8={fp8}")
-    c = Case(9200 + M, M, N, 1024, 24, 6, "random", fp8)
+@pytest.mark.parametrize("M,N,R", [(40, 320, 24), (64, 4096, 24), (100, 320, 48), (300, 520, 24)])
+def test_an_adapter_with_nan_and_inf_reaches_its_own_rows_alone(M, N, R, fp8):
+    announce(f"lora wild adapter M={M} N={N} R={R} fp8={fp8}")
+    c = Case(9200 + M, M, N, 1024, R, 6, "random", fp8)
     Lb = c.Lb.clone()
     Lb[2, ::7, 3] = float("nan")
     Lb[2, 1::7, 20] = float("inf")
@@ -148,6 +149,14 @@ def test_an_adapter_with_nan_and_inf_reaches_its_own_rows_alone(M, N, fp8):
     D = c.run(Lb=Lb)
     assert D.isnan().any() and D.isinf().any()
     c.check(D, Lb)
+    clean = c.run()
+    La = c.La.clone()
+    La[3, 7, 100] = float("nan")
+    La[3, R - 1, 1000] = float("inf")
+    D = c.run(La=La)
+    mine = torch.from_numpy(c.ids == 3)
+    assert D.cpu()[mine].isnan().all() and not D.cpu()[~mine].isnan().any()
+    c.check(torch.where(mine.to(DEV)[:, None], clean, D))
 
 
 def test_a_row_with_nan_and_inf_reaches_itself_alone():

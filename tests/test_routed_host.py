@@ -211,9 +211,10 @@ def test_lora_validation(lib):
     assert fp8(sa=NUL) == fp8(X=NUL) == INVALID
     assert fp8(X=P_ODD) == MISALIGNED
     assert fp8(K=20608) == SHAPE
-    assert lib.lora_workspace(0, 128, 16) == lib.lora_workspace(4, 128, 0) == 0
-    assert lib.lora_workspace(4, 128, 16) >= 4 * 16 * 2
-    assert lib.lora_workspace(4096, 7168, 64) > 4096 * 64 * 2
+    for fp8 in (0, 1):
+        assert lib.lora_workspace(0, 64, 128, 16, fp8) == lib.lora_workspace(4, 64, 128, 0, fp8) == 0
+        assert lib.lora_workspace(4, 64, 128, 16, fp8) >= 4 * 16 * 4 + 4 * 64 * 4
+        assert lib.lora_workspace(4096, 64, 7168, 64, fp8) > 4096 * 64 * 2
 
 
 def test_lora_reference_is_the_dense_sum():
