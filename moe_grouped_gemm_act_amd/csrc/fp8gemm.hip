@@ -610,8 +610,27 @@ __device__ __forceinline__ void store_bf16(const v4f (&acc)[TN][TM], uint16_t *D
 constexpr int LORA_MAXG = 4096;
 constexpr int LORA_BLOCKS = 1, LORA_DOTS = 2;
 
-// One wave lists the distinct adapters of the tile's BM rows in ascending
-// order (a bitmap over all lg) while the loaders fetch the first blocks.
+// LDS words for the loader waves.  The compiler lets an LDS read of its own wait
+// for every direct-to-LDS load in flight (they might write what it reads), which
+// would drain the ring at each adapter block.
+__device__ __forceinline__ uint32_t lds_at(const void *p) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
+}
+__device__ __forceinline__ int lds_word(uint32_t at) {
+  int v;
+  asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(at) : "memory");
+  return v;
+}
+// the words at `at` and 128 bytes on
+__device__ __forceinline__ u32x2 lds_word_pair(uint32_t at) {
+  u32x2 v;
+  asm volatile("ds_read2_b32 %0, %1 offset0:0 offset1:32\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(at) : "memory");
+  return v;
+}
+
+// One compute wave lists the distinct adapters of the tile's BM rows in
+// ascending order (a bitmap over all lg) while the loaders fetch the first
+// blocks; the barrier of the first block publishes the list.
 template <int BM>
 __device__ __forceinline__ void adapter_list(const Args &a, int m0, int lane, int *s_id, int *s_list,
                                              uint32_t *s_bits, int *s_n) {
@@ -642,8 +661,8 @@ __device__ __forceinline__ void adapter_list(const Args &a, int m0, int lane, in
 
 // An adapter block of a compute wave: ranks e0 .. e0 + 63 of the added K axis.
 // A row's zeros beside an infinite or NaN weight of another row's adapter would
-// make NaN, so a block whose weights hold one is done without the MFMA, each
-// output from the ranks of its own row's adapter alone.
+// make NaN, so those weights are left out of the matrix product and their
+// products added to the rows of their own adapter, one weight at a time.
 template <int TN, int TM, int BM>
 __device__ __forceinline__ void adapter_kblock(const uint8_t *sl, int e0, int R, int n_list, const int *s_id,
                                                const int *s_list, int wn, int wm, int fr, int fg,
@@ -652,50 +671,55 @@ __device__ __forceinline__ void adapter_kblock(const uint8_t *sl, int e0, int R,
   const uint8_t *pa = sl + wm * TM * 16 * BK, *pb = sl + (BM + wn * TN * 16) * BK;
   constexpr int G = 16 * BK;  // bytes per 16-row group
   bf16_peak peak;
-  {
-    v8i bfr[TN];
+  v8i bfr[TN];
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      bfr[i] = frag_at(pb + i * G + lo, pb + i * G + hi);
-      peak.see(__builtin_bit_cast(u32x4, bf_half(bfr[i], 0)));
-      peak.see(__builtin_bit_cast(u32x4, bf_half(bfr[i], 1)));
-    }
-    if (__ballot(!peak.finite()) == 0) {
-#pragma unroll
-      for (int j = 0; j < TM; ++j) {
-        asm volatile("" ::: "memory");  // one activation fragment at a time
-        const v8i afr = frag_at(pa + j * G + lo, pa + j * G + hi);
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int i = 0; i < TN; ++i)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf_half(bfr[i], h), bf_half(afr, h),
-                                                                acc[i][j], 0, 0, 0);
-      }
-      return;
-    }
+  for (int i = 0; i < TN; ++i) {
+    bfr[i] = frag_at(pb + i * G + lo, pb + i * G + hi);
+    peak.see(__builtin_bit_cast(u32x4, bf_half(bfr[i], 0)));
+    peak.see(__builtin_bit_cast(u32x4, bf_half(bfr[i], 1)));
   }
-  // each output from the ranks of its own row's adapter alone, read from the
-  // slot (rolled loops: the accumulators leave few registers)
+  const bool wild = __ballot(!peak.finite()) != 0;
+  if (wild) {
+#pragma unroll
+    for (int i = 0; i < TN; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t w = (uint32_t)bfr[i][e];
+        bfr[i][e] = (int)(((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) |
+                          ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u));
+      }
+  }
 #pragma unroll
   for (int j = 0; j < TM; ++j) {
-    const int row = (wm * TM + j) * 16 + fr, id = s_id[row];
+    asm volatile("" ::: "memory");  // one activation fragment at a time
+    const v8i afr = frag_at(pa + j * G + lo, pa + j * G + hi);
 #pragma unroll
-    for (int i = 0; i < TN; ++i) {
-      const int wr = BM + (wn * TN + i) * 16 + 4 * fg;
-#pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        const int li = (e0 + 8 * c) / R;
-        if (li >= n_list || s_list[li] != id) continue;
-        const uint16_t *h = reinterpret_cast<const uint16_t *>(sl + row * BK + chunk_pos(c, row));
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint16_t *w = reinterpret_cast<const uint16_t *>(sl + (wr + r) * BK + chunk_pos(c, wr + r));
+      for (int i = 0; i < TN; ++i)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf_half(bfr[i], h), bf_half(afr, h), acc[i][j], 0, 0, 0);
+  }
+  if (!wild) return;
+  // the weights left out, one after the other
 #pragma unroll 1
-          for (int e = 0; e < 8; ++e)
-            acc[i][j][r] = __builtin_fmaf(__uint_as_float((uint32_t)h[e] << 16),
-                                          __uint_as_float((uint32_t)w[e] << 16), acc[i][j][r]);
-        }
+  for (int n = 0; n < TN * 16; ++n) {
+    const int row = BM + wn * TN * 16 + n;
+#pragma unroll 1
+    for (int e = 0; e < 64; ++e) {
+      const uint32_t w = *reinterpret_cast<const uint16_t *>(sl + row * BK + chunk_pos(e >> 3, row) + (e & 7) * 2);
+      const int li = (e0 + e) / R;
+      if ((w & 0x7F80u) != 0x7F80u || li >= n_list) continue;
+      const int ad = s_list[li];
+#pragma unroll
+      for (int j = 0; j < TM; ++j) {
+        const int m = (wm * TM + j) * 16 + fr;
+        const uint32_t h = *reinterpret_cast<const uint16_t *>(sl + m * BK + chunk_pos(e >> 3, m) + (e & 7) * 2);
+        const float v = __uint_as_float(h << 16) * __uint_as_float(w << 16);
+        const bool mine = s_id[m] == ad && fg == (n & 15) >> 2;
+#pragma unroll
+        for (int i = 0; i < TN; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[i][j][r] += mine && i == n >> 4 && r == (n & 3) ? v : 0.f;
       }
     }
   }
@@ -790,14 +814,14 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
   const int kb0 = split * kbps, nk = max(0, min(Kb - kb0, kbps));
   // LORA: this item's share of the tile's adapter blocks (its K split's part):
   // the first and how many; valid once the list is (one barrier later)
-  auto adapter_blocks = [&](int &first) {
-    const int n = (s_ln * a.lr + 63) / 64, parts = tail ? a.tail_splits : S;
+  auto adapter_blocks = [&](int adapters, int &first) {
+    const int n = (adapters * a.lr + 63) / 64, parts = tail ? a.tail_splits : S;
     first = n * split / parts;
     return n * (split + 1) / parts - first;
   };
   // the loaders' first loads are all of the base product: they need not wait
   // for the list, which the first block's barrier then publishes
-  const bool list_first = LORA && nk < STAGES - 1;
+  const bool list_first = LORA && nk < STAGES;
 
   const uint8_t *A = a.A, *B = a.B;
   const float *sa = a.sa, *sb = a.sb;
@@ -870,30 +894,38 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
     const __amdgpu_buffer_rsrc_t rlh = LORA ? rsrc(a.lh, (uint32_t)M * a.lr * 2) : ra;
     const __amdgpu_buffer_rsrc_t rlb = LORA ? rsrc(a.lb, (uint32_t)a.lg * N * a.lr * 2) : rb;
     // adapter block t >= nk (blocks past nt load nothing); as many loads as a base block
+    int adapters = 0;  // of the tile, once the list is there
     auto adapter_block = [&](int t, uint8_t *sl) {
       const int col = (lane & 7) ^ row_key(L * 8 + (lane >> 3));  // the same for every q: NLD is even
-      const int e = (lb0 + t - nk) * 64 + col * 8, li = e / a.lr, rank = e - li * a.lr;
-      const bool live = t < nt && li < s_ln;
-      const int ad = live ? s_llist[live ? li : 0] : -2;
+      const uint32_t e = (uint32_t)(lb0 + t - nk) * 64 + col * 8, li = e / (uint32_t)a.lr, rank = e - li * a.lr;
+      const bool live = t < nt && li < (uint32_t)adapters;
+      const int listed = lds_word(lds_at(s_llist) + (live ? li * 4 : 0)), ad = live ? listed : -2;
+      const int r0 = L * 8 + (lane >> 3);  // the q-th row is r0 + 8 NLD q
+      static_assert(!LORA || (NLD == 4 && QA % 2 == 0), "two ids, 32 rows apart, at a time");
 #pragma unroll
-      for (int q = 0; q < DMA; ++q) {
-        const int r = (L + NLD * q) * 8 + (lane >> 3);
-        uint32_t o = OOB;
-        if (q < QA) {
-          if (s_lid[LORA ? r : 0] == ad) o = ((uint32_t)(m0 + r) * a.lr + rank) * 2;
-        } else {
-          const int grow = n0 + r - BM;
-          if (live && grow < N) o = (((uint32_t)ad * N + grow) * a.lr + rank) * 2;
-        }
-        dma16(q < QA ? rlh : rlb, o, sl + (L + NLD * q) * 1024);
+      for (int q = 0; q < QA; q += 2) {
+        const u32x2 id = lds_word_pair(lds_at(s_lid) + (r0 + 8 * NLD * q) * 4);
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          dma16(rlh, (int)id[p] == ad ? ((uint32_t)(m0 + r0 + 8 * NLD * (q + p)) * a.lr + rank) * 2 : OOB,
+                sl + (L + NLD * (q + p)) * 1024);
+      }
+#pragma unroll
+      for (int q = QA; q < DMA; ++q) {
+        const int grow = n0 + r0 + 8 * NLD * q - BM;
+        dma16(rlb, live && grow < N ? (((uint32_t)ad * N + grow) * a.lr + rank) * 2 : OOB, sl + (L + NLD * q) * 1024);
       }
 #pragma unroll
       for (int jj = 0; jj < SPL; ++jj) dma4(rs, OOB, sl + sdst[jj]);
     };
-    if (LORA && list_first) {
-      __builtin_amdgcn_s_barrier();  // the list
-      asm volatile("" ::: "memory");
-      nt = nk + adapter_blocks(lb0);
+    if constexpr (LORA) {
+      if (list_first) {
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();  // the list
+        asm volatile("" ::: "memory");
+        adapters = lds_word(lds_at(&s_ln));
+        nt = nk + adapter_blocks(adapters, lb0);
+      }
     }
     // G(t): K block kb0 + t (clamped: blocks past the range re-read the last
     // one and are never consumed) -> slot t % STAGES
@@ -901,30 +933,54 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
   do {                                                                                        \
     const int kb_ = kb0 + min((t), nk - 1);                                                   \
     uint8_t *sl_ = lds[(t) % STAGES];                                                         \
-    if (LORA && (t) >= nk) {                                                                  \
-      adapter_block((t), sl_);                                                                \
-      break;                                                                                  \
-    }                                                                                         \
     _Pragma("unroll") for (int q = 0; q < DMA; ++q)                                          \
         dma16(q < QA ? ra : rb, off[q] + (uint32_t)kb_ * BK, sl_ + (L + NLD * q) * 1024);     \
     _Pragma("unroll") for (int jj = 0; jj < SPL; ++jj)                                        \
         dma4(rs, soff[jj] + (uint32_t)kb_ * M * 4, sl_ + sdst[jj]);                           \
   } while (0)
-    if (nk > 0) {
+    if (nk > 0 && !list_first) {
 #pragma unroll
       for (int t = 0; t < STAGES - 1; ++t) TK_G(t);
     }
-    for (int t0 = 0; t0 < nt; t0 += STAGES) {
+    if constexpr (LORA) {
+      // the base blocks that are followed by base blocks STAGES - 1 later, as
+      // below; then a rolled loop that loads adapter blocks (once in the code,
+      // which has to stay within the instruction cache)
+      if (list_first) {
+        for (int t = 0; t < nk; ++t) TK_G(t);
+#pragma unroll 1
+        for (int t = nk; t < STAGES - 1; ++t) adapter_block(t, lds[t]);
+      }
+    }
+    int done = 0;  // blocks handed over
+    const int plain = LORA ? nk - (STAGES - 1) : nk;
+    for (int t0 = 0; t0 < plain; t0 += STAGES) {
 #pragma unroll
       for (int u = 0; u < STAGES; ++u) {
         const int t = t0 + u;
-        if (t >= nt) break;
+        if (t >= plain) break;
         __builtin_amdgcn_s_waitcnt(vmcnt_imm(PER_G * (STAGES - 2)));  // my loads of block t landed
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();  // ... and everyone's; all compute waves are past block t - 1
         asm volatile("" ::: "memory");
-        if (LORA && t == 0 && !list_first) nt = nk + adapter_blocks(lb0);
         TK_G(t + STAGES - 1);
+        if (LORA) done = t + 1;
+      }
+    }
+    if constexpr (LORA) {
+      if (!list_first) {  // nk >= STAGES: the first barrier has passed
+        adapters = lds_word(lds_at(&s_ln));
+        nt = nk + adapter_blocks(adapters, lb0);
+      }
+      int slot = (done + STAGES - 1) % STAGES;
+#pragma unroll 1
+      for (int t = done; t < nt; ++t) {
+        __builtin_amdgcn_s_waitcnt(vmcnt_imm(PER_G * (STAGES - 2)));
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_s_barrier();
+        asm volatile("" ::: "memory");
+        adapter_block(t + STAGES - 1, lds[slot]);
+        slot = slot + 1 == STAGES ? 0 : slot + 1;
       }
     }
 #undef TK_G
@@ -935,9 +991,10 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
 
   // ---------------- compute waves ----------------
   const int wn = wave % WGN, wm = wave / WGN;
-  if (LORA) {
-    if (wave == 0) adapter_list<LORA ? BM : 64>(a, m0, lane, s_lid, s_llist, s_lbits, &s_ln);
-    __builtin_amdgcn_s_waitcnt(0);  // written before the barrier that publishes it
+  if constexpr (LORA) {
+    // the last compute wave: the weight scales' preload below takes the first ones
+    if (wave == NCW - 1) adapter_list<BM>(a, m0, lane, s_lid, s_llist, s_lbits, &s_ln);
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // written before the barrier that publishes it
     if (list_first) {
       asm volatile("" ::: "memory");
       __builtin_amdgcn_s_barrier();
@@ -1011,7 +1068,7 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
   }
   if constexpr (LORA) {
     int first;
-    const int n = adapter_blocks(first);
+    const int n = adapter_blocks(s_ln, first);
     int slot = nk % STAGES;
     for (int t = 0; t < n; ++t) {
       asm volatile("" ::: "memory");

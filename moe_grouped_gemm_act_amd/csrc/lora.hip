@@ -303,7 +303,7 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
 
 // H from the partial planes, summed in order; JOIN planes' loads at a time (those
 // past the last read zeros)
-constexpr int JOIN = 16;
+template <int JOIN>
 __global__ __launch_bounds__(256) void lora_join_kernel(const float *planes, const int32_t *ids,
                                                         const float *scale, uint16_t *H, int M, int R, int G,
                                                         int n) {
@@ -386,7 +386,9 @@ int shrink(const void *X, const void *La, const int32_t *ids, const float *scale
   const int st = launch(f, dim3(p.tiles, p.ry, p.planes), WAVES * 64, args, stream);
   if (st != FP8GEMM_OK || p.planes == 1) return st;
   void *jargs[] = {&planes, &ids, &scale, &H, &M, &R, &G, &p.planes};
-  return launch(reinterpret_cast<const void *>(&lora_join_kernel),
+  return launch(p.planes <= 4    ? reinterpret_cast<const void *>(&lora_join_kernel<4>)
+                : p.planes <= 8  ? reinterpret_cast<const void *>(&lora_join_kernel<8>)
+                                 : reinterpret_cast<const void *>(&lora_join_kernel<16>),
                 dim3((unsigned)(((long long)M * (R / 4) + 255) / 256)), 256, jargs, stream);
 }
 
