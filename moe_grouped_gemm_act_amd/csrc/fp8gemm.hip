@@ -58,6 +58,7 @@
 #include "bf16.h"
 #include "e4m3.h"
 #include "fp8gemm.h"
+#include "lds_asm.h"
 #include "lora.h"
 #include "lora_dot.h"
 
@@ -609,24 +610,6 @@ __device__ __forceinline__ void store_bf16(const v4f (&acc)[TN][TM], uint16_t *D
 // kernel joins the planes and h Lb^T (lora.hip).
 constexpr int LORA_MAXG = 4096;
 constexpr int LORA_BLOCKS = 1, LORA_DOTS = 2;
-
-// LDS words for the loader waves.  The compiler lets an LDS read of its own wait
-// for every direct-to-LDS load in flight (they might write what it reads), which
-// would drain the ring at each adapter block.
-__device__ __forceinline__ uint32_t lds_at(const void *p) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const void *)p;
-}
-__device__ __forceinline__ int lds_word(uint32_t at) {
-  int v;
-  asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(at) : "memory");
-  return v;
-}
-// the words at `at` and 128 bytes on
-__device__ __forceinline__ u32x2 lds_word_pair(uint32_t at) {
-  u32x2 v;
-  asm volatile("ds_read2_b32 %0, %1 offset0:0 offset1:32\n\ts_waitcnt lgkmcnt(0)" : "=&v"(v) : "v"(at) : "memory");
-  return v;
-}
 
 // One compute wave lists the distinct adapters of the tile's BM rows in
 // ascending order (a bitmap over all lg) while the loaders fetch the first

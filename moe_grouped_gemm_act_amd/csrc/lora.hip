@@ -25,6 +25,7 @@
 
 #include "bf16.h"
 #include "fp8gemm_routed.h"
+#include "lds_asm.h"
 #include "lora.h"
 #include "lora_dot.h"
 
@@ -148,6 +149,11 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *planes, i
 constexpr int WAVES = 4, MT = 4, ROWS = MT * 16;
 constexpr int ring_stages(int rt) { return rt <= 2 ? 3 : 2; }  // 4 waves' rings within 144 KB
 
+__device__ __forceinline__ v4f mfma(u32x4 a, u32x4 b, v4f c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
+                                                 0, 0, 0);
+}
+
 __device__ __forceinline__ int row_key(int row) { return (row >> 1) & 7; }
 
 // dst: partial planes [gridDim.z][M][R] (fp32), or with one plane H itself
@@ -199,12 +205,12 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
       ++pq;
     }
     if (pq >= n) return;
-    const int ad = s_list[pq];
+    const int ad = __builtin_amdgcn_readfirstlane(lds_word(lds_at(s_list) + pq * 4));
     rl = rsrc(La + ((size_t)ad * R + r0) * K, (uint32_t)min(RT * 16, R - r0) * K * 2);
 #pragma unroll
     for (int i = 0; i < MT * 2; ++i) {
       const int r = i * 8 + (lane >> 3);
-      off[i] = s_id[r] == ad ? (uint32_t)r * K * 2 + ((i & 1) ? col ^ 64 : col) : OOB;
+      off[i] = lds_word(lds_at(s_id) + r * 4) == ad ? (uint32_t)r * K * 2 + ((i & 1) ? col ^ 64 : col) : OOB;
     }
   };
   auto produce = [&]() {  // past the last pair: nothing is loaded
@@ -229,26 +235,19 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
   for (int s = 0; s < STAGES - 1; ++s) produce();
   int slot = 0;
   for (int e = wave; e < n * nkb; e += WAVES) {
-    __builtin_amdgcn_s_waitcnt(0xC07F);  // the last block's fragments are in registers: its slot is free
-    asm volatile("" ::: "memory");
-    produce();
+    produce();  // into the slot of the block before, whose fragments are in registers
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(PER * (STAGES - 1)));  // this block has landed
     asm volatile("" ::: "memory");
-    const uint8_t *sl = ring[wave] + slot * SLOT;
+    const uint32_t sl = lds_at(ring[wave]) + slot * SLOT;
     slot = slot + 1 == STAGES ? 0 : slot + 1;
-    bf16x8 a[MT][2], b[RT][2];
+    u32x4 a[MT][2], b[RT][2];
+    lds_fragments<MT>(sl + lo, sl + hi, a);
+    lds_fragments<RT>(sl + MT * 2048 + lo, sl + MT * 2048 + hi, b);
     bf16_peak peak;
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      a[j][0] = *reinterpret_cast<const bf16x8 *>(sl + j * 2048 + lo);
-      a[j][1] = *reinterpret_cast<const bf16x8 *>(sl + j * 2048 + hi);
-    }
-#pragma unroll
     for (int i = 0; i < RT; ++i) {
-      b[i][0] = *reinterpret_cast<const bf16x8 *>(sl + (MT + i) * 2048 + lo);
-      b[i][1] = *reinterpret_cast<const bf16x8 *>(sl + (MT + i) * 2048 + hi);
-      peak.see(__builtin_bit_cast(u32x4, b[i][0]));
-      peak.see(__builtin_bit_cast(u32x4, b[i][1]));
+      peak.see(b[i][0]);
+      peak.see(b[i][1]);
     }
     if (__ballot(!peak.finite()) == 0) {
 #pragma unroll
@@ -257,7 +256,7 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
         for (int i = 0; i < RT; ++i)
 #pragma unroll
           for (int j = 0; j < MT; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i][h], a[j][h], acc[i][j], 0, 0, 0);
+            acc[i][j] = mfma(b[i][h], a[j][h], acc[i][j]);
     } else {
       const int ad = s_list[e / nkb];
 #pragma unroll
@@ -266,8 +265,8 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           v4f p = {0.f, 0.f, 0.f, 0.f};
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i][0], a[j][0], p, 0, 0, 0);
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[i][1], a[j][1], p, 0, 0, 0);
+          p = mfma(b[i][0], a[j][0], p);
+          p = mfma(b[i][1], a[j][1], p);
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[i][j][r] += mine ? p[r] : 0.f;
         }
