@@ -14,7 +14,7 @@
 //     nothing when the rows name different adapters and little while they are
 //     few.
 //   * M R <= LORA_DOT: the same dot products in a launch of their own.
-//   * more rows: 64 rows x RT 16 ranks a workgroup on the matrix cores, K
+//   * more rows: 16 or 64 rows x RT 16 ranks a workgroup on the matrix cores, K
 //     split over workgroups until they fill the chip; the fp32 partial planes
 //     are summed in order by a second, small kernel.
 
@@ -136,7 +136,7 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *planes, i
 }
 
 // ---- more rows ---------------------------------------------------------------
-// A workgroup lists its 64 rows' distinct adapters and takes a range of K
+// A workgroup lists the distinct adapters of its MT x 16 rows and takes a range of K
 // blocks (64 elements).  Its work is the sequence of all (adapter, block)
 // pairs, which its four waves take in turn.  A row is zero in the blocks of
 // every adapter but its own, so all of them add into the same accumulators and
@@ -146,8 +146,11 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *planes, i
 // rows x 128 bytes each, swizzled as the tile kernel's) into a ring of its own,
 // STAGES - 1 blocks ahead, with no barrier in the loop.  Rows of other
 // adapters are out-of-range loads: zeros, no traffic.
-constexpr int WAVES = 4, MT = 4, ROWS = MT * 16;
-constexpr int ring_stages(int rt) { return rt <= 2 ? 3 : 2; }  // 4 waves' rings within 144 KB
+constexpr int WAVES = 4;
+// within 144 KB for the four rings, and 63 loads in flight a wave
+constexpr int ring_stages(int rt, int mt) {
+  return mt == 4 ? (rt <= 2 ? 3 : 2) : rt == 1 ? 8 : rt == 2 ? 6 : rt == 3 ? 4 : 3;
+}
 
 __device__ __forceinline__ v4f mfma(u32x4 a, u32x4 b, v4f c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c,
@@ -157,12 +160,12 @@ __device__ __forceinline__ v4f mfma(u32x4 a, u32x4 b, v4f c) {
 __device__ __forceinline__ int row_key(int row) { return (row >> 1) & 7; }
 
 // dst: partial planes [gridDim.z][M][R] (fp32), or with one plane H itself
-template <int RT>
+template <int RT, int MT>
 __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t *X, const uint16_t *La,
                                                                  const int32_t *ids, const float *scale,
                                                                  uint16_t *H, float *planes, int M, int K,
                                                                  int R, int G, int tiles, int kb_per) {
-  constexpr int STAGES = ring_stages(RT);
+  constexpr int STAGES = ring_stages(RT, MT), ROWS = MT * 16;
   constexpr int TR = (MT + RT) * 16, SLOT = TR * 128, PER = TR / 8;
   static_assert(PER * STAGES < 64, "loads in flight must fit vmcnt");
   static_assert(RT * MT * 1024 <= STAGES * SLOT, "partial tiles reuse the rings");
@@ -175,9 +178,9 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
   const int x = blockIdx.x % 8, tile = x * (tiles / 8) + min(x, tiles % 8) + blockIdx.x / 8;
   const int m0 = tile * ROWS, r0 = blockIdx.y * RT * 16;
   if (wave == 0) {
-    int id = m0 + lane < M ? ids[m0 + lane] : -1;
+    int id = lane < ROWS && m0 + lane < M ? ids[m0 + lane] : -1;
     if (id < 0 || id >= G) id = -1;
-    s_id[lane] = id;
+    if (lane < ROWS) s_id[lane] = id;
     unsigned long long rest = __ballot(id >= 0);
     int n = 0;
     while (rest) {  // one turn per distinct adapter
@@ -282,8 +285,9 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
     for (int j = 0; j < MT; ++j) part[(i * MT + j) * 64 + lane] = acc[i][j];
   __syncthreads();
 #pragma unroll
-  for (int e = 0; e < RT * MT / WAVES; ++e) {
-    const int p = wave * (RT * MT / WAVES) + e;
+  for (int e = 0; e < (RT * MT + WAVES - 1) / WAVES; ++e) {
+    const int p = e * WAVES + wave;
+    if (p >= RT * MT) break;
     v4f s = reinterpret_cast<const v4f *>(ring[0])[p * 64 + lane];
 #pragma unroll
     for (int v = 1; v < WAVES; ++v) s += reinterpret_cast<const v4f *>(ring[v])[p * 64 + lane];
@@ -332,6 +336,10 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const float *planes, con
 // 20.7; 64 x 7168 x 2048 FP8 rank 64 (2^24.8) 18.6 and 34.2 | 14.6 and 15.3;
 // 128 x 24576 x 1536 FP8 rank 16 (2^25.6) 32.4 and 26.8 | 23.6 and 16.4.
 constexpr int LORA_DOT = 8192;
+// Rows up to which the matrix form takes them 16 at a time: a tile then holds
+// few adapters however they are mixed, and reading an adapter once per tile
+// still costs little.
+constexpr int LORA_NARROW = 1024;
 constexpr long long LORA_FEW = 1LL << 25;
 
 bool few_rows(int M, int N, int R) {
@@ -340,14 +348,15 @@ bool few_rows(int M, int N, int R) {
 
 struct ShrinkPlan {
   bool dot;
-  int rt, tiles, ry, planes, kb_per;
+  int mt, rt, tiles, ry, planes, kb_per;
 };
 
 ShrinkPlan shrink_plan(int M, int K, int R) {
   ShrinkPlan p{};
   p.dot = (long long)M * R <= LORA_DOT;
   p.rt = std::min(4, (R + 15) / 16);
-  p.tiles = (M + ROWS - 1) / ROWS;
+  p.mt = M <= LORA_NARROW ? 1 : 4;
+  p.tiles = (M + p.mt * 16 - 1) / (p.mt * 16);
   p.ry = (R + p.rt * 16 - 1) / (p.rt * 16);
   // K blocks shared out until 256 workgroups run, at least one block a wave
   const int nkb = K / 64;
@@ -378,10 +387,14 @@ int shrink(const void *X, const void *La, const int32_t *ids, const float *scale
     return launch(f, dim3((R + DOT_WAVES - 1) / DOT_WAVES, M), DOT_WAVES * 64, args, stream);
   }
   void *args[] = {&X, &La, &ids, &scale, &H, &planes, &M, &K, &R, &G, &p.tiles, &p.kb_per};
-  const void *f = p.rt == 1   ? reinterpret_cast<const void *>(&lora_shrink_kernel<1>)
-                  : p.rt == 2 ? reinterpret_cast<const void *>(&lora_shrink_kernel<2>)
-                  : p.rt == 3 ? reinterpret_cast<const void *>(&lora_shrink_kernel<3>)
-                              : reinterpret_cast<const void *>(&lora_shrink_kernel<4>);
+#define SHRINK(rt_)                                                                             \
+  case rt_:                                                                                      \
+    f = p.mt == 1 ? reinterpret_cast<const void *>(&lora_shrink_kernel<rt_, 1>)                  \
+                  : reinterpret_cast<const void *>(&lora_shrink_kernel<rt_, 4>);                 \
+    break;
+  const void *f = nullptr;
+  switch (p.rt) { SHRINK(1) SHRINK(2) SHRINK(3) SHRINK(4) }
+#undef SHRINK
   const int st = launch(f, dim3(p.tiles, p.ry, p.planes), WAVES * 64, args, stream);
   if (st != FP8GEMM_OK || p.planes == 1) return st;
   void *jargs[] = {&planes, &ids, &scale, &H, &M, &R, &G, &p.planes};

@@ -106,6 +106,7 @@ SHAPES = [  # M, N, K, R, G
     (128, 24600, 128, 16, 33), (129, 257, 256, 16, 7), (300, 1030, 512, 40, 3), (515, 2112, 384, 128, 12),
     (200, 150, 960, 64, 3), (257, 300, 7168, 48, 2), (600, 70, 2048, 16, 300), (150, 64, 1024, 200, 5),
     (16, 300, 512, 128, 5), (2, 4099, 256, 1024, 3), (30, 1000, 128, 64, 7), (9, 500, 256, 40, 4), (33, 2112, 640, 32, 33),
+    (1030, 64, 512, 16, 3), (1500, 72, 1024, 64, 5), (1027, 48, 1984, 40, 30), (2100, 33, 320, 32, 9),
     (1100, 3700, 256, 64, 4096),
 ]
 
