@@ -94,8 +94,8 @@ int moe_sort_masked(const int32_t *ids, int32_t *row, int32_t *masked_m, int32_t
  *   moe_dispatch_fp8: its 1x128 quantisation, the codes and scales that
  *     quantize_fp8_1x128 gives, bit for bit: A [G][M,H] codes,
  *     sa [G][H/128][M].  H % 128 == 0.
- * Constraints: k >= 1; T k, G M and T below 2^31 (tensors may be larger than
- * 2^31 bytes); X and A 16-byte aligned, sa and row 4-byte.  T == 0 or H == 0
+ * Constraints: k >= 1; T k and G M below 2^31, H below 2^29 (tensors may be
+ * larger than 2^31 bytes); X and A 16-byte aligned, sa and row 4-byte.  T == 0 or H == 0
  * returns FP8GEMM_OK.
  */
 int moe_dispatch_bf16(const void *X, const int32_t *row, void *A, int T, int H, int k, int M, int G,
@@ -118,7 +118,7 @@ int moe_combine_bf16(const void *Y, const int32_t *row, const float *w, void *ou
  * Its gradients, from dout [T,H] (bf16): dY[row[t,j]] = w[t,j] dout[t] (bf16;
  * rows that no choice names keep their previous contents) and
  * dw[t,j] = sum_h dout[t,h] Y[row[t,j],h] (fp32; 0 where row[t,j] is outside
- * [0,M)).  Constraints of both: k >= 1; T k, M below 2^31; dout, Y, dY and out
+ * [0,M)).  Constraints of both: k >= 1; T k and M below 2^31, H below 2^29; dout, Y, dY and out
  * 16-byte aligned, the others 4-byte; dY is not Y.
  */
 int moe_combine_backward_bf16(const void *dout, const void *Y, const int32_t *row, const float *w,

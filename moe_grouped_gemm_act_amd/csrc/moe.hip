@@ -520,17 +520,45 @@ int sort(const int32_t *ids, int32_t *row, int32_t *m_indices, int32_t *counts, 
 }
 
 // ---- tokens to rows and back -----------------------------------------------
-constexpr int ROW_THREADS = 256;
+constexpr int ROW_THREADS = 256, ROW_WAVES = ROW_THREADS / 64;
 
-// The token of a workgroup of a (pieces of a row, T) grid: workgroups go round
+// The piece of a token's row of a wave (64 V elements): workgroups go round
 // robin to the 8 XCDs, and each XCD takes a run of consecutive tokens, so
-// neighbouring rows and scales of an expert are written from one L2.
-__device__ __forceinline__ void token_piece(int T, int pieces, int &t, int &piece) {
-  const int n = T * pieces, b = blockIdx.x;
+// neighbouring rows and scales of an expert are written from one L2.  False
+// past the last.
+__device__ __forceinline__ bool token_piece(int T, int pieces, int &t, int &piece) {
+  const int n = gridDim.x, b = blockIdx.x;
   const int x = b % 8, per = n / 8, rem = n % 8;
-  const int item = x * per + min(x, rem) + b / 8;
+  const int item = (x * per + min(x, rem) + b / 8) * ROW_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   t = item / pieces;
   piece = item % pieces;
+  return t < T;
+}
+
+// Row r of a tensor of rows of H bf16 values as a buffer; a row that is not
+// there is an empty one, whose loads give zeros and whose stores are dropped, so
+// the choices' accesses need no branches between them and are issued together.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const uint16_t *p, int r, int rows, int H) {
+  const bool ok = r >= 0 && r < rows;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p + (ok ? (size_t)r * H : 0)), 0,
+                                           ok ? H * 2 : 0, 0x00020000);
+}
+constexpr int NT = 2;  // non-temporal
+template <int V>
+__device__ __forceinline__ u32x4 load_piece(__amdgpu_buffer_rsrc_t r, uint32_t off, bool nt) {
+  if (V == 1) return u32x4{(uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0), 0, 0, 0};
+  return __builtin_bit_cast(u32x4, nt ? __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, NT)
+                                      : __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+}
+template <int V>
+__device__ __forceinline__ void store_piece(__amdgpu_buffer_rsrc_t r, uint32_t off, u32x4 v) {
+  if (V == 1) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v[0], r, off, 0, 0);
+  else __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
+}
+// element i of a piece
+template <int V>
+__device__ __forceinline__ float piece_at(const u32x4 &v, int i) {
+  return (i & 1) ? bf16_hi(v[i / 2]) : bf16_lo(v[i / 2]);
 }
 
 // V elements per thread: 8 (16 bytes) where H allows, else 1.  Plain stores: the
@@ -542,23 +570,11 @@ __global__ __launch_bounds__(ROW_THREADS) void dispatch_bf16_kernel(const uint16
                                                                     uint16_t *A, int T, int H, int k,
                                                                     int rows, int pieces) {
   int t, piece;
-  token_piece(T, pieces, t, piece);
-  const int h = (piece * ROW_THREADS + threadIdx.x) * V;
-  if (h >= H) return;
+  if (!token_piece(T, pieces, t, piece)) return;
+  const uint32_t off = (uint32_t)(piece * 64 + (threadIdx.x & 63)) * V * 2;  // past the row: dropped
+  const u32x4 v = load_piece<V>(row_buffer(X, t, T, H), off, false);
   const int32_t *rt = row + (size_t)t * k;
-  if (V == 8) {
-    const u32x4 v = *reinterpret_cast<const u32x4 *>(X + (size_t)t * H + h);
-    for (int j = 0; j < k; ++j) {
-      const int r = rt[j];
-      if (r >= 0 && r < rows) *reinterpret_cast<u32x4 *>(A + (size_t)r * H + h) = v;
-    }
-  } else {
-    const uint16_t v = X[(size_t)t * H + h];
-    for (int j = 0; j < k; ++j) {
-      const int r = rt[j];
-      if (r >= 0 && r < rows) A[(size_t)r * H + h] = v;
-    }
-  }
+  for (int j = 0; j < k; ++j) store_piece<V>(row_buffer(A, rt[j], rows, H), off, v);
 }
 
 // 16 elements per thread, 8 threads per 128-wide block: the block is quantised
@@ -569,8 +585,8 @@ __global__ __launch_bounds__(ROW_THREADS) void dispatch_fp8_kernel(const uint16_
                                                                    uint8_t *A, float *sa, int T, int H,
                                                                    int k, int M, int rows, int pieces) {
   int t, piece;
-  token_piece(T, pieces, t, piece);
-  const int h = (piece * ROW_THREADS + threadIdx.x) * 16;
+  if (!token_piece(T, pieces, t, piece)) return;
+  const int h = (piece * 64 + (threadIdx.x & 63)) * 16;
   if (h >= H) return;  // whole 8-thread groups: H is a multiple of 128
   const u32x4 *src = reinterpret_cast<const u32x4 *>(X + (size_t)t * H + h);
   const u32x4 v[2] = {src[0], src[1]};
@@ -603,99 +619,80 @@ __global__ __launch_bounds__(ROW_THREADS) void dispatch_fp8_kernel(const uint16_
 }
 
 // Y is read once and not again: non-temporal loads (4095 x 4096 tokens from 8
-// rows each 63 -> 55 us).
-template <int V>
+// rows each 63 -> 55 us).  KB choices at a time.
+template <int V, int KB>
 __global__ __launch_bounds__(ROW_THREADS) void combine_kernel(const uint16_t *Y, const int32_t *row,
                                                               const float *w, uint16_t *out, int T,
                                                               int H, int k, int M, int pieces) {
   int t, piece;
-  token_piece(T, pieces, t, piece);
-  const int h = (piece * ROW_THREADS + threadIdx.x) * V;
-  if (h >= H) return;
+  if (!token_piece(T, pieces, t, piece)) return;
+  const uint32_t off = (uint32_t)(piece * 64 + (threadIdx.x & 63)) * V * 2;
   const int32_t *rt = row + (size_t)t * k;
-  const float *wt = w + (size_t)t * k;
   float acc[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) acc[i] = 0.f;
-#pragma unroll 4
-  for (int j = 0; j < k; ++j) {
-    const int r = rt[j];
-    if (r < 0 || r >= M) continue;
-    const float f = w ? wt[j] : 1.f;
-    if (V == 8) {
-      const u32x4 y = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(Y + (size_t)r * H + h));
+  for (int j0 = 0; j0 < k; j0 += KB) {
+    u32x4 y[KB];
+    float f[KB];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[(2 * i) % V] = __builtin_fmaf(f, bf16_lo(y[i]), acc[(2 * i) % V]);
-        acc[(2 * i + 1) % V] = __builtin_fmaf(f, bf16_hi(y[i]), acc[(2 * i + 1) % V]);
-      }
-    } else {
-      acc[0] = __builtin_fmaf(f, __uint_as_float((uint32_t)Y[(size_t)r * H + h] << 16), acc[0]);
+    for (int j = 0; j < KB; ++j) {
+      const int r = j0 + j < k ? rt[j0 + j] : -1;
+      y[j] = load_piece<V>(row_buffer(Y, r, M, H), off, true);
+      f[j] = r < 0 || r >= M ? 0.f : w ? w[(size_t)t * k + j0 + j] : 1.f;  // not the weight of a missing row
     }
+#pragma unroll
+    for (int j = 0; j < KB; ++j)
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(f[j], piece_at<V>(y[j], i), acc[i]);
   }
+  u32x4 o = {bf16_of(acc[0]), 0, 0, 0};
   if (V == 8) {
-    u32x4 o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = bf16_pair(acc[(2 * i) % V], acc[(2 * i + 1) % V]);
-    *reinterpret_cast<u32x4 *>(out + (size_t)t * H + h) = o;
-  } else {
-    out[(size_t)t * H + h] = (uint16_t)bf16_of(acc[0]);
   }
+  store_piece<V>(row_buffer(out, t, T, H), off, o);
 }
 
-// One workgroup per token.  Eight choices at a time share one reading of dout;
+// One workgroup per token.  KB choices at a time share one reading of dout;
 // their products with Y are summed per thread, then over the wave and, through
-// LDS, over the four waves in order.
-template <int V>
+// LDS, over the four waves in order.  Plain access: with non-temporal stores
+// this and the product that reads dY took 1-6% longer together.
+template <int V, int KB>
 __global__ __launch_bounds__(ROW_THREADS) void combine_backward_kernel(const uint16_t *dout,
                                                                        const uint16_t *Y,
                                                                        const int32_t *row, const float *w,
                                                                        uint16_t *dY, float *dw, int T,
                                                                        int H, int k, int M) {
-  constexpr int KB = 8, WAVES = ROW_THREADS / 64;
-  __shared__ float s_dot[WAVES][KB];
-  int t, piece;
-  token_piece(T, 1, t, piece);
+  __shared__ float s_dot[ROW_WAVES][KB];
+  const int x = blockIdx.x % 8, t = x * (T / 8) + min(x, T % 8) + blockIdx.x / 8;  // as token_piece
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const __amdgpu_buffer_rsrc_t rd = row_buffer(dout, t, T, H);
   for (int j0 = 0; j0 < k; j0 += KB) {
     float dot[KB], f[KB];
-    int r[KB];
+    __amdgpu_buffer_rsrc_t ry[KB], rg[KB];
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
+      const int r = j0 + j < k ? row[(size_t)t * k + j0 + j] : -1;
+      ry[j] = row_buffer(Y, r, M, H);
+      rg[j] = row_buffer(dY, r, M, H);
+      f[j] = j0 + j < k ? w[(size_t)t * k + j0 + j] : 0.f;
       dot[j] = 0.f;
-      r[j] = -1;
-      f[j] = 0.f;
-      if (j0 + j < k) {
-        r[j] = row[(size_t)t * k + j0 + j];
-        if (r[j] >= M) r[j] = -1;
-        f[j] = w[(size_t)t * k + j0 + j];
-      }
     }
-    for (int h = threadIdx.x * V; h < H; h += ROW_THREADS * V) {
-      if (V == 8) {
-        const u32x4 d = *reinterpret_cast<const u32x4 *>(dout + (size_t)t * H + h);
+    for (uint32_t off = threadIdx.x * V * 2; off < (uint32_t)H * 2; off += ROW_THREADS * V * 2) {
+      const u32x4 d = load_piece<V>(rd, off, false);
+      u32x4 y[KB];
 #pragma unroll
-        for (int j = 0; j < KB; ++j) {
-          if (r[j] < 0) continue;
-          const u32x4 y = *reinterpret_cast<const u32x4 *>(Y + (size_t)r[j] * H + h);
-          u32x4 o;
+      for (int j = 0; j < KB; ++j) y[j] = load_piece<V>(ry[j], off, false);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            dot[j] = __builtin_fmaf(bf16_lo(d[i]), bf16_lo(y[i]), dot[j]);
-            dot[j] = __builtin_fmaf(bf16_hi(d[i]), bf16_hi(y[i]), dot[j]);
-            o[i] = bf16_pair(f[j] * bf16_lo(d[i]), f[j] * bf16_hi(d[i]));
-          }
-          *reinterpret_cast<u32x4 *>(dY + (size_t)r[j] * H + h) = o;
+      for (int j = 0; j < KB; ++j) {
+        u32x4 o = {bf16_of(f[j] * piece_at<V>(d, 0)), 0, 0, 0};
+        if (V == 8) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = bf16_pair(f[j] * bf16_lo(d[i]), f[j] * bf16_hi(d[i]));
         }
-      } else {
-        const float d = __uint_as_float((uint32_t)dout[(size_t)t * H + h] << 16);
+        store_piece<V>(rg[j], off, o);
 #pragma unroll
-        for (int j = 0; j < KB; ++j) {
-          if (r[j] < 0) continue;
-          const size_t at = (size_t)r[j] * H + h;
-          dot[j] = __builtin_fmaf(d, __uint_as_float((uint32_t)Y[at] << 16), dot[j]);
-          dY[at] = (uint16_t)bf16_of(f[j] * d);
-        }
+        for (int i = 0; i < V; ++i) dot[j] = __builtin_fmaf(piece_at<V>(d, i), piece_at<V>(y[j], i), dot[j]);
       }
     }
     if (j0 > 0) __syncthreads();  // the group before has been read
@@ -708,27 +705,31 @@ __global__ __launch_bounds__(ROW_THREADS) void combine_backward_kernel(const uin
     if ((int)threadIdx.x < KB && j0 + (int)threadIdx.x < k) {
       float s = 0.f;
 #pragma unroll
-      for (int v = 0; v < WAVES; ++v) s += s_dot[v][threadIdx.x];
-      dw[(size_t)t * k + j0 + threadIdx.x] = s;  // 0 for a choice without a row
+      for (int v = 0; v < ROW_WAVES; ++v) s += s_dot[v][threadIdx.x];
+      const int r = row[(size_t)t * k + j0 + threadIdx.x];
+      dw[(size_t)t * k + j0 + threadIdx.x] = r < 0 || r >= M ? 0.f : s;
     }
   }
 }
 
+constexpr int MAX_H = 1 << 29;  // a row's bytes fit a buffer
+
 int check_rows(const void *P, const void *Q, const int32_t *row, int T, int H, int k, int M, int G) {
   if (T < 0 || H < 0 || k < 1 || M < 0 || G < 1) return FP8GEMM_INVALID_ARG;
   if (T == 0 || H == 0) return -1;
-  if ((long long)T * k >= LIM || (long long)G * M >= LIM || H > LIM - ROW_THREADS * 16)
+  if ((long long)T * k >= LIM || (long long)G * M >= LIM || H >= MAX_H)
     return FP8GEMM_UNSUPPORTED_SHAPE;
   if (!P || !Q || !row) return FP8GEMM_INVALID_ARG;
   if (!aligned(P, 16) || !aligned(Q, 16) || !aligned(row, 4)) return FP8GEMM_MISALIGNED;
   return FP8GEMM_OK;
 }
 
-// pieces of a row for V elements a thread; false if the grid would be too large
+// pieces of a row for V elements a lane; false if the grid would be too large
 bool row_pieces(int T, int H, int V, int &pieces, dim3 &grid) {
-  pieces = (int)(((long long)H + (long long)ROW_THREADS * V - 1) / (ROW_THREADS * V));
-  if ((long long)T * pieces >= LIM) return false;
-  grid = dim3((unsigned)(T * pieces));
+  pieces = (H + 64 * V - 1) / (64 * V);
+  const long long waves = (long long)T * pieces;
+  if (waves >= LIM - ROW_WAVES) return false;
+  grid = dim3((unsigned)((waves + ROW_WAVES - 1) / ROW_WAVES));
   return true;
 }
 
@@ -821,25 +822,29 @@ int moe_combine_bf16(const void *Y, const int32_t *row, const float *w, void *ou
   dim3 grid;
   if (!row_pieces(T, H, vec ? 8 : 1, pieces, grid)) return FP8GEMM_UNSUPPORTED_SHAPE;
   void *args[] = {&Y, &row, &w, &out, &T, &H, &k, &M, &pieces};
-  return launch(vec ? reinterpret_cast<const void *>(&combine_kernel<8>)
-                    : reinterpret_cast<const void *>(&combine_kernel<1>),
-                grid, dim3(ROW_THREADS), args, stream);
+  const void *f = !vec     ? reinterpret_cast<const void *>(&combine_kernel<1, 8>)
+                  : k <= 2 ? reinterpret_cast<const void *>(&combine_kernel<8, 2>)
+                  : k <= 4 ? reinterpret_cast<const void *>(&combine_kernel<8, 4>)
+                           : reinterpret_cast<const void *>(&combine_kernel<8, 8>);
+  return launch(f, grid, dim3(ROW_THREADS), args, stream);
 }
 
 int moe_combine_backward_bf16(const void *dout, const void *Y, const int32_t *row, const float *w,
                               void *dY, float *dw, int T, int H, int k, int M, void *stream) {
   if (T < 0 || H < 0 || k < 1 || M < 0) return FP8GEMM_INVALID_ARG;
   if (T == 0) return FP8GEMM_OK;
-  if ((long long)T * k >= LIM || H > LIM - ROW_THREADS * 8) return FP8GEMM_UNSUPPORTED_SHAPE;
+  if ((long long)T * k >= LIM || H >= MAX_H) return FP8GEMM_UNSUPPORTED_SHAPE;
   if (!row || !w || !dw || (H > 0 && (!dout || (M > 0 && (!Y || !dY || dY == Y)))))
     return FP8GEMM_INVALID_ARG;  // H == 0 writes dw alone
   if (!aligned(dout, 16) || !aligned(Y, 16) || !aligned(dY, 16) || !aligned(row, 4) || !aligned(w, 4) ||
       !aligned(dw, 4))
     return FP8GEMM_MISALIGNED;
   void *args[] = {&dout, &Y, &row, &w, &dY, &dw, &T, &H, &k, &M};
-  return launch(H % 8 == 0 ? reinterpret_cast<const void *>(&combine_backward_kernel<8>)
-                           : reinterpret_cast<const void *>(&combine_backward_kernel<1>),
-                dim3(T), dim3(ROW_THREADS), args, stream);
+  const void *f = H % 8 != 0 ? reinterpret_cast<const void *>(&combine_backward_kernel<1, 8>)
+                  : k <= 2   ? reinterpret_cast<const void *>(&combine_backward_kernel<8, 2>)
+                  : k <= 4   ? reinterpret_cast<const void *>(&combine_backward_kernel<8, 4>)
+                             : reinterpret_cast<const void *>(&combine_backward_kernel<8, 8>);
+  return launch(f, dim3(T), dim3(ROW_THREADS), args, stream);
 }
 
 }  // extern "C"

@@ -100,9 +100,19 @@ def _typed(t, dtype, name):
     return t
 
 
-def _out(t, shape, dtype, device, name):
-    if t is None:
+def _empty(shape, dtype, device, stream):
+    """Memory of the stream that the call runs on: what the caching allocator
+    hands out there is free for that stream's next kernel, and what is freed
+    there is used again after this call's kernels."""
+    if stream is None:
         return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _out(t, shape, dtype, device, name, stream):
+    if t is None:
+        return _empty(shape, dtype, device, stream)
     _shape(_typed(t, dtype, name), shape, name)
     return t
 
@@ -117,8 +127,8 @@ def moe_topk(logits, k, renormalize=True, scale=1.0, ids=None, w=None, stream=No
     f32 = logits.dtype == torch.float32
     if not f32:
         _typed(logits, torch.bfloat16, "logits")
-    ids = _out(ids, (T, k), torch.int32, logits.device, "ids")
-    w = _out(w, (T, k), torch.float32, logits.device, "w")
+    ids = _out(ids, (T, k), torch.int32, logits.device, "ids", stream)
+    w = _out(w, (T, k), torch.float32, logits.device, "w", stream)
     dev = _dev(logits, ids, w)
     lib = _load()
     _check((lib.moe_topk_f32 if f32 else lib.moe_topk_bf16)(
@@ -137,7 +147,7 @@ def moe_topk_backward(logits, ids, w, dw, renormalize=True, scale=1.0, dlogits=N
     _shape(_typed(ids, torch.int32, "ids"), (T, k), "ids")
     _shape(_typed(w, torch.float32, "w"), (T, k), "w")
     _shape(_typed(dw, torch.float32, "dw"), (T, k), "dw")
-    dlogits = _out(dlogits, (T, E), logits.dtype, logits.device, "dlogits")
+    dlogits = _out(dlogits, (T, E), logits.dtype, logits.device, "dlogits", stream)
     dev = _dev(logits, ids, w, dw, dlogits)
     lib = _load()
     _check((lib.moe_topk_backward_f32 if f32 else lib.moe_topk_backward_bf16)(
@@ -155,9 +165,7 @@ def _workspace(lib, S, G, device, stream):
     n = lib.moe_sort_workspace(S, G)
     if n == 0:
         return None, None
-    ws = torch.empty(n, dtype=torch.int32, device=device)
-    if stream is not None:
-        ws.record_stream(stream)  # freed on return; the caching allocator waits for that stream
+    ws = _empty(n, torch.int32, device, stream)
     return ws, _p(ws)
 
 
@@ -172,9 +180,9 @@ def moe_sort_contiguous(ids, G, M=None, row=None, m_indices=None, counts=None, s
     lib = _load()
     if M is None:
         M = lib.moe_contiguous_rows(S, G)
-    row = _out(row, ids.shape, torch.int32, at, "row")
-    m_indices = _out(m_indices, (M,), torch.int32, at, "m_indices")
-    counts = _out(counts, (G,), torch.int32, at, "counts")
+    row = _out(row, ids.shape, torch.int32, at, "row", stream)
+    m_indices = _out(m_indices, (M,), torch.int32, at, "m_indices", stream)
+    counts = _out(counts, (G,), torch.int32, at, "counts", stream)
     dev = _dev(_typed(ids, torch.int32, "ids"), row, m_indices, counts)
     ws, wp = _workspace(lib, S, G, at, stream)
     _check(lib.moe_sort_contiguous(_p(ids), _p(row), _p(m_indices), _p(counts), wp, S, G, M,
@@ -189,8 +197,8 @@ def moe_sort_masked(ids, G, M, row=None, masked_m=None, stream=None):
     S = ids.numel()
     at = ids.device
     lib = _load()
-    row = _out(row, ids.shape, torch.int32, at, "row")
-    masked_m = _out(masked_m, (G,), torch.int32, at, "masked_m")
+    row = _out(row, ids.shape, torch.int32, at, "row", stream)
+    masked_m = _out(masked_m, (G,), torch.int32, at, "masked_m", stream)
     dev = _dev(_typed(ids, torch.int32, "ids"), row, masked_m)
     ws, wp = _workspace(lib, S, G, at, stream)
     _check(lib.moe_sort_masked(_p(ids), _p(row), _p(masked_m), wp, S, G, M, _stream(stream, dev)))
@@ -213,7 +221,7 @@ def moe_dispatch_bf16(X, row, rows, A=None, stream=None):
     lead, M, G = _rows(rows)
     k = row.shape[1]
     _shape(_typed(row, torch.int32, "row"), (T, k), "row")
-    A = _out(A, (*lead, H), torch.bfloat16, X.device, "A")
+    A = _out(A, (*lead, H), torch.bfloat16, X.device, "A", stream)
     dev = _dev(_typed(X, torch.bfloat16, "X"), row, A)
     _check(_load().moe_dispatch_bf16(_p(X), _p(row), _p(A), T, H, k, M, G, _stream(stream, dev)))
     return A
@@ -228,8 +236,8 @@ def moe_dispatch_fp8(X, row, rows, A=None, sa=None, stream=None):
     k = row.shape[1]
     _shape(_typed(row, torch.int32, "row"), (T, k), "row")
     A = _codes(A, "A") if A is not None else None
-    A = _out(A, (*lead, H), torch.uint8, X.device, "A")
-    sa = _out(sa, (*lead[:-1], H // 128, M), torch.float32, X.device, "sa")
+    A = _out(A, (*lead, H), torch.uint8, X.device, "A", stream)
+    sa = _out(sa, (*lead[:-1], H // 128, M), torch.float32, X.device, "sa", stream)
     dev = _dev(_typed(X, torch.bfloat16, "X"), row, A, sa)
     _check(_load().moe_dispatch_fp8(_p(X), _p(row), _p(A), _p(sa), T, H, k, M, G,
                                     _stream(stream, dev)))
@@ -249,7 +257,7 @@ def moe_combine(Y, row, w=None, out=None, stream=None):
     M, H = _flat(Y)
     T, k = row.shape
     _typed(row, torch.int32, "row")
-    out = _out(out, (T, H), torch.bfloat16, Y.device, "out")
+    out = _out(out, (T, H), torch.bfloat16, Y.device, "out", stream)
     if w is not None:
         _shape(_typed(w, torch.float32, "w"), (T, k), "w")
         dev = _dev(_typed(Y, torch.bfloat16, "Y"), row, w, out)
@@ -275,8 +283,8 @@ def moe_combine_backward(dout, Y, row, w, dY=None, dw=None, stream=None):
     _typed(row, torch.int32, "row")
     _shape(_typed(dout, torch.bfloat16, "dout"), (T, H), "dout")
     _shape(_typed(w, torch.float32, "w"), (T, k), "w")
-    dY = _out(dY, Y.shape, torch.bfloat16, Y.device, "dY")
-    dw = _out(dw, (T, k), torch.float32, Y.device, "dw")
+    dY = _out(dY, Y.shape, torch.bfloat16, Y.device, "dY", stream)
+    dw = _out(dw, (T, k), torch.float32, Y.device, "dw", stream)
     dev = _dev(_typed(Y, torch.bfloat16, "Y"), dout, row, w, dY, dw)
     _check(_load().moe_combine_backward_bf16(_p(dout), _p(Y), _p(row), _p(w), _p(dY), _p(dw), T, H,
                                              k, M, _stream(stream, dev)))
@@ -292,9 +300,7 @@ def _adapters(base, X, M, K, N, La, Lb, ids, scale, D, stream):
     _shape(_typed(ids, torch.int32, "ids"), (M,), "ids")
     _shape(_typed(scale, torch.float32, "scale"), (G,), "scale")
     dev = _dev(*base, La, Lb, ids, scale, D)
-    ws = torch.empty(_load().lora_workspace(M, N, K, R, len(base) == 5), dtype=torch.uint8, device=D.device)
-    if stream is not None:
-        ws.record_stream(stream)  # freed on return; the caching allocator waits for that stream
+    ws = _empty(_load().lora_workspace(M, N, K, R, len(base) == 5), torch.uint8, D.device, stream)
     return R, G, dev, ws
 
 
@@ -306,7 +312,7 @@ def gemm_bf16_nt_lora(A, B, La, Lb, ids, scale, D=None, stream=None):
     M, K = A.shape
     N = B.shape[0]
     _shape(_typed(B, torch.bfloat16, "B"), (N, K), "B")
-    D = _out(D, (M, N), torch.bfloat16, A.device, "D")
+    D = _out(D, (M, N), torch.bfloat16, A.device, "D", stream)
     R, G, dev, ws = _adapters((A, B), A, M, K, N, La, Lb, ids, scale, D, stream)
     _check(_load().gemm_bf16_nt_lora(_p(A), _p(B), _p(La), _p(Lb), _p(ids), _p(scale), _p(D), _p(ws),
                                      M, N, K, R, G, _stream(stream, dev)))
@@ -323,7 +329,7 @@ def gemm_fp8_1x128_128x128_bf16_lora(A, sa, B, sb, X, La, Lb, ids, scale, D=None
     _shape(B, (N, K), "B")
     _shape(_typed(sa, torch.float32, "sa"), (K // 128, M), "sa")
     _shape(_typed(sb, torch.float32, "sb"), ((N + 127) // 128, K // 128), "sb")
-    D = _out(D, (M, N), torch.bfloat16, A.device, "D")
+    D = _out(D, (M, N), torch.bfloat16, A.device, "D", stream)
     R, G, dev, ws = _adapters((A, sa, B, sb, X), X, M, K, N, La, Lb, ids, scale, D, stream)
     _check(_load().gemm_fp8_1x128_128x128_bf16_lora(
         _p(A), _p(sa), _p(B), _p(sb), _p(X), _p(La), _p(Lb), _p(ids), _p(scale), _p(D), _p(ws),
