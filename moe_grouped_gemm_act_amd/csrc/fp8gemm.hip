@@ -958,11 +958,13 @@ __global__ __launch_bounds__((WGN * WGM + NLD) * 64) void tile_kernel(Args a) {
       int slot = (done + STAGES - 1) % STAGES;
 #pragma unroll 1
       for (int t = done; t < nt; ++t) {
-        __builtin_amdgcn_s_waitcnt(vmcnt_imm(PER_G * (STAGES - 2)));
+        // near the end fewer blocks are in flight
+        if (t + STAGES - 2 < nt) __builtin_amdgcn_s_waitcnt(vmcnt_imm(PER_G * (STAGES - 2)));
+        else __builtin_amdgcn_s_waitcnt(vmcnt_imm(0));
         asm volatile("" ::: "memory");
         __builtin_amdgcn_s_barrier();
         asm volatile("" ::: "memory");
-        adapter_block(t + STAGES - 1, lds[slot]);
+        if (t + STAGES - 1 < nt) adapter_block(t + STAGES - 1, lds[slot]);
         slot = slot + 1 == STAGES ? 0 : slot + 1;
       }
     }

@@ -66,7 +66,9 @@ __global__ __launch_bounds__(DOT_WAVES * 64) void lora_dot_kernel(const uint16_t
 // A wave takes B x 64 columns of one row.  P lanes (a power of two) share a
 // column's ranks, 8 (16 bytes) a lane and turn, so a load instruction reads
 // 1 KB of Lb in a row; the column's sum then goes to one lane of the P, chosen
-// so that the 64 lanes end with the 64 columns of a batch.
+// so that the 64 lanes end with the 64 columns of a batch.  Bound by reading Lb
+// and by the launch: 64 rows x 7168 columns of 64 adapters of rank 16 4.3 us
+// (14.7 MB of Lb, 1.8 MB of planes), one row x 4096 2.6-3.8 us.
 template <int P, int B>
 __global__ __launch_bounds__(256) void lora_expand_kernel(const float *planes, int n_planes, const float *h,
                                                           const uint16_t *Lb, const int32_t *ids,
@@ -136,16 +138,19 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *planes, i
 }
 
 // ---- more rows ---------------------------------------------------------------
-// A workgroup lists the distinct adapters of its MT x 16 rows and takes a range of K
-// blocks (64 elements).  Its work is the sequence of all (adapter, block)
-// pairs, which its four waves take in turn.  A row is zero in the blocks of
-// every adapter but its own, so all of them add into the same accumulators and
-// the waves' partial tiles meet once, in LDS, at the end.  (Zero times an
-// infinite or NaN weight would reach other adapters' rows: a block that holds
-// one adds to its own rows alone.)  A wave feeds itself: direct-to-LDS loads (8
-// rows x 128 bytes each, swizzled as the tile kernel's) into a ring of its own,
-// STAGES - 1 blocks ahead, with no barrier in the loop.  Rows of other
+// A workgroup takes MT x 16 rows, RT x 16 ranks and a range of K blocks (64
+// elements).  Its work is the sequence of all (adapter, block) pairs of its
+// rows' distinct adapters, which its four waves take in turn.  A row is zero in
+// the blocks of every adapter but its own, so all of them add into the same
+// accumulators and the waves' partial tiles meet once, in LDS, at the end.  (Zero
+// times an infinite or NaN weight would reach other adapters' rows: a block that
+// holds one adds to its own rows alone.)  A wave feeds itself: direct-to-LDS loads
+// (8 rows x 128 bytes each, swizzled as the tile kernel's) into a ring of its
+// own, STAGES - 1 blocks ahead, with no barrier in the loop.  Rows of other
 // adapters are out-of-range loads: zeros, no traffic.
+// Bound by reading X once from HBM and by the pipeline's start: 4096 x 7168 of 12
+// requests, rank 64, 22.5 us (73 MB); 777 x 7168 of 5, rank 32, 8-10 us; 4096 x 1536,
+// rank 64, 11.4 us.
 constexpr int WAVES = 4;
 // within 144 KB for the four rings, and 63 loads in flight a wave
 constexpr int ring_stages(int rt, int mt) {
@@ -159,7 +164,7 @@ __device__ __forceinline__ v4f mfma(u32x4 a, u32x4 b, v4f c) {
 
 __device__ __forceinline__ int row_key(int row) { return (row >> 1) & 7; }
 
-// dst: partial planes [gridDim.z][M][R] (fp32), or with one plane H itself
+// to partial planes [gridDim.z][M][R] (fp32), or with one plane to H itself
 template <int RT, int MT>
 __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t *X, const uint16_t *La,
                                                                  const int32_t *ids, const float *scale,
@@ -170,29 +175,26 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
   static_assert(PER * STAGES < 64, "loads in flight must fit vmcnt");
   static_assert(RT * MT * 1024 <= STAGES * SLOT, "partial tiles reuse the rings");
   __shared__ __attribute__((aligned(1024))) uint8_t ring[WAVES][STAGES * SLOT];
-  __shared__ int s_id[ROWS], s_list[ROWS], s_n;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fg = lane >> 4;
   // each XCD takes a run of consecutive row tiles, which often share adapters
   const int x = blockIdx.x % 8, tile = x * (tiles / 8) + min(x, tiles % 8) + blockIdx.x / 8;
   const int m0 = tile * ROWS, r0 = blockIdx.y * RT * 16;
-  if (wave == 0) {
-    int id = lane < ROWS && m0 + lane < M ? ids[m0 + lane] : -1;
-    if (id < 0 || id >= G) id = -1;
-    if (lane < ROWS) s_id[lane] = id;
-    unsigned long long rest = __ballot(id >= 0);
-    int n = 0;
-    while (rest) {  // one turn per distinct adapter
-      const int ad = (int)lane_of((uint32_t)id, __builtin_ctzll(rest));
-      if (lane == 0) s_list[n] = ad;
-      ++n;
-      rest &= ~__ballot(id == ad);
-    }
-    if (lane == 0) s_n = n;
-  }
-  __syncthreads();
-  const int n = s_n, kb0 = blockIdx.z * kb_per, nkb = min(K / 64, kb0 + kb_per) - kb0;
+  // lane r holds row r's adapter and its scale; every wave lists them for itself
+  int id = lane < ROWS && m0 + lane < M ? ids[m0 + lane] : -1;
+  if (id < 0 || id >= G) id = -1;
+  const unsigned long long named = __ballot(id >= 0);
+  const float row_scale = id >= 0 ? scale[id] : 0.f;
+  // the adapter of the lowest row left, whose rows are then taken away
+  auto next = [&](unsigned long long &rest) {
+    const int ad = (int)lane_of((uint32_t)id, __builtin_ctzll(rest));
+    rest &= ~__ballot(id == ad);
+    return ad;
+  };
+  int n = 0;
+  for (unsigned long long rest = named; rest; ++n) next(rest);
+  const int kb0 = blockIdx.z * kb_per, nkb = min(K / 64, kb0 + kb_per) - kb0;
   if (n == 0) return;
   const __amdgpu_buffer_rsrc_t rx = rsrc(X + (size_t)m0 * K, (uint32_t)min(ROWS, M - m0) * K * 2);
   __amdgpu_buffer_rsrc_t rl = rx;
@@ -201,19 +203,22 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
 #pragma unroll
   for (int i = MT * 2; i < PER; ++i)  // row_key(r) = row_key(r % 8) ^ 4 where r / 8 is odd
     off[i] = (uint32_t)(i * 8 + (lane >> 3) - ROWS) * K * 2 + ((i & 1) ? col ^ 64 : col);
-  int pq = 0, pk = wave, pslot = 0;  // the producer's adapter (place in the list), block and slot
-  auto aim = [&]() {                 // its addresses for a new adapter
+  // the producer: its block, slot, adapter's number and the rows of the adapters
+  // after it
+  int pk = wave, pslot = 0, pq = 0;
+  unsigned long long prest = named;
+  int pad = next(prest);
+  auto aim = [&]() {  // its addresses for a new adapter
     while (pk >= nkb && pq < n) {
       pk -= nkb;
-      ++pq;
+      if (++pq < n) pad = next(prest);
     }
     if (pq >= n) return;
-    const int ad = __builtin_amdgcn_readfirstlane(lds_word(lds_at(s_list) + pq * 4));
-    rl = rsrc(La + ((size_t)ad * R + r0) * K, (uint32_t)min(RT * 16, R - r0) * K * 2);
+    rl = rsrc(La + ((size_t)pad * R + r0) * K, (uint32_t)min(RT * 16, R - r0) * K * 2);
 #pragma unroll
     for (int i = 0; i < MT * 2; ++i) {
       const int r = i * 8 + (lane >> 3);
-      off[i] = lds_word(lds_at(s_id) + r * 4) == ad ? (uint32_t)r * K * 2 + ((i & 1) ? col ^ 64 : col) : OOB;
+      off[i] = __shfl(id, r, 64) == pad ? (uint32_t)r * K * 2 + ((i & 1) ? col ^ 64 : col) : OOB;
     }
   };
   auto produce = [&]() {  // past the last pair: nothing is loaded
@@ -236,8 +241,14 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
   aim();
 #pragma unroll
   for (int s = 0; s < STAGES - 1; ++s) produce();
-  int slot = 0;
-  for (int e = wave; e < n * nkb; e += WAVES) {
+  int slot = 0, ck = wave, cad;  // the consumer's block and adapter
+  unsigned long long crest = named;
+  cad = next(crest);
+  for (int e = wave; e < n * nkb; e += WAVES, ck += WAVES) {
+    while (ck >= nkb) {
+      ck -= nkb;
+      cad = next(crest);
+    }
     produce();  // into the slot of the block before, whose fragments are in registers
     __builtin_amdgcn_s_waitcnt(vmcnt_imm(PER * (STAGES - 1)));  // this block has landed
     asm volatile("" ::: "memory");
@@ -261,10 +272,9 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
           for (int j = 0; j < MT; ++j)
             acc[i][j] = mfma(b[i][h], a[j][h], acc[i][j]);
     } else {
-      const int ad = s_list[e / nkb];
 #pragma unroll
       for (int j = 0; j < MT; ++j) {
-        const bool mine = s_id[j * 16 + fr] == ad;
+        const bool mine = __shfl(id, j * 16 + fr, 64) == cad;
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
           v4f p = {0.f, 0.f, 0.f, 0.f};
@@ -292,20 +302,20 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(const uint16_t 
 #pragma unroll
     for (int v = 1; v < WAVES; ++v) s += reinterpret_cast<const v4f *>(ring[v])[p * 64 + lane];
     // ranks 4 fg .. 4 fg + 3 of the i-th 16, row fr of the j-th
-    const int i = p / MT, m = p % MT * 16 + fr, r = r0 + i * 16 + 4 * fg, ad = s_id[m];
-    if (ad < 0 || r >= R) continue;  // R is a multiple of 8
+    const int i = p / MT, m = p % MT * 16 + fr, r = r0 + i * 16 + 4 * fg;
+    const float f = __shfl(row_scale, m, 64);
+    if (!((named >> m) & 1) || r >= R) continue;  // R is a multiple of 8
     const size_t at = (size_t)(m0 + m) * R + r;
     if (gridDim.z > 1) {
       *reinterpret_cast<v4f *>(planes + (size_t)blockIdx.z * M * R + at) = s;
     } else {
-      const float f = scale[ad];
       *reinterpret_cast<u32x2 *>(H + at) = u32x2{bf16_pair(f * s[0], f * s[1]), bf16_pair(f * s[2], f * s[3])};
     }
   }
 }
 
 // H from the partial planes, summed in order; JOIN planes' loads at a time (those
-// past the last read zeros)
+// past the last read zeros).  A launch and a round trip: 4-5 us at 4096 x 64 x 4 planes.
 template <int JOIN>
 __global__ __launch_bounds__(256) void lora_join_kernel(const float *planes, const int32_t *ids,
                                                         const float *scale, uint16_t *H, int M, int R, int G,
@@ -313,8 +323,7 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const float *planes, con
   const uint32_t q = blockIdx.x * 256 + threadIdx.x;
   const int m = (int)(q / (uint32_t)(R / 4));
   if (m >= M) return;
-  const int ad = ids[m];
-  if (ad < 0 || ad >= G) return;
+  int ad = ids[m];  // asked for beside the planes, not before them
   const uint32_t plane = (uint32_t)M * R * 4;
   const __amdgpu_buffer_rsrc_t r = rsrc(planes, plane * n);
   v4f s = {0.f, 0.f, 0.f, 0.f};
@@ -325,6 +334,7 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const float *planes, con
 #pragma unroll
     for (int i = 0; i < JOIN; ++i) s += __builtin_bit_cast(v4f, p[i]);
   }
+  if (ad < 0 || ad >= G) return;  // such a row's planes hold anything
   const float f = scale[ad];
   *reinterpret_cast<u32x2 *>(H + (size_t)q * 4) = u32x2{bf16_pair(f * s[0], f * s[1]), bf16_pair(f * s[2], f * s[3])};
 }
@@ -338,7 +348,8 @@ __global__ __launch_bounds__(256) void lora_join_kernel(const float *planes, con
 constexpr int LORA_DOT = 8192;
 // Rows up to which the matrix form takes them 16 at a time: a tile then holds
 // few adapters however they are mixed, and reading an adapter once per tile
-// still costs little.
+// still costs little (whole products, 16 and 64 rows a tile: 150 x 7168 x 2048 FP8
+// rank 64, rows all of different adapters, 54 and 134 us; of three, 29 and 31).
 constexpr int LORA_NARROW = 1024;
 constexpr long long LORA_FEW = 1LL << 25;
 
@@ -351,16 +362,36 @@ struct ShrinkPlan {
   int mt, rt, tiles, ry, planes, kb_per;
 };
 
+// The matrix form's tiles.  Without a K split the join and its launch (5-6 us with
+// the gap before it) fall away, which pays while a workgroup's share of X and La
+// stays under 330 KB: tiles small enough to make 192 workgroups, if any are
+// (first factor and join, in us: 4096 x 1536 rank 64 11.4 against 16.1 split;
+// 1000 x 2048 rank 16 8.9 and 14.0; 777 x 7168 rank 32, 459 KB, 19.9 and 16.3).
 ShrinkPlan shrink_plan(int M, int K, int R) {
   ShrinkPlan p{};
   p.dot = (long long)M * R <= LORA_DOT;
-  p.rt = std::min(4, (R + 15) / 16);
-  p.mt = M <= LORA_NARROW ? 1 : 4;
-  p.tiles = (M + p.mt * 16 - 1) / (p.mt * 16);
-  p.ry = (R + p.rt * 16 - 1) / (p.rt * 16);
-  // K blocks shared out until 256 workgroups run, at least one block a wave
-  const int nkb = K / 64;
-  // (so the planes hold at most 256 tiles of 64 x 64: 4 MB)
+  const int r16 = (R + 15) / 16, nkb = K / 64;
+  auto tile = [&](int mt, int rt) {
+    p.mt = mt;
+    p.rt = rt;
+    p.tiles = (M + mt * 16 - 1) / (mt * 16);
+    p.ry = (r16 + rt - 1) / rt;
+    return (long long)p.tiles * p.ry;
+  };
+  const bool narrow = M <= LORA_NARROW;
+  for (int mt = narrow ? 1 : 4; mt >= 1; mt -= 3) {
+    int rt = std::min(4, r16);
+    while (rt > 1 && tile(mt, rt) < 192) --rt;
+    if (tile(mt, rt) >= 192) break;
+  }
+  if ((long long)(p.mt + p.rt) * 16 * K * 2 <= 330 * 1024) {
+    p.planes = 1;
+    p.kb_per = nkb;
+    return p;
+  }
+  tile(narrow ? 1 : 4, std::min(4, r16));
+  // K blocks shared out until 256 workgroups run, at least one block a wave (so
+  // the planes hold at most 256 tiles of 64 x 64: 4 MB)
   const int want = (int)std::max(1LL, 256LL / ((long long)p.tiles * p.ry));
   p.planes = std::max(1, std::min(want, nkb / WAVES));
   p.kb_per = nkb > 0 ? (nkb + p.planes - 1) / p.planes : 0;

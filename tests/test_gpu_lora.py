@@ -207,9 +207,11 @@ def test_deterministic_and_independent_of_the_batch():
 
 
 def test_streams_and_graph_replay():
-    for M, N, K, fp8 in ((64, 4096, 7168, False), (64, 2112, 7168, True), (300, 1030, 1024, True)):
-        announce(f"lora graph {M}x{N}x{K} fp8={fp8}")
-        c = Case(9600 + M, M, N, K, 16, 8, "random", fp8)
+    # few rows; a K split in the library's workspace; the matrix form, with and without planes to join
+    for M, N, K, R, fp8 in ((64, 4096, 7168, 16, False), (64, 2112, 7168, 16, True), (128, 2112, 2048, 128, True),
+                            (128, 2112, 2048, 128, False), (300, 1030, 1024, 40, True), (400, 520, 7168, 64, False)):
+        announce(f"lora graph {M}x{N}x{K} rank {R} fp8={fp8}")
+        c = Case(9600 + M, M, N, K, R, 8, "random", fp8)
         X, t = c.X.to(DEV), torch.from_numpy
         rest = [c.La.to(DEV), c.Lb.to(DEV), t(c.ids).to(DEV), t(c.scale).to(DEV)]
         D = sentinel_out((M, N))
