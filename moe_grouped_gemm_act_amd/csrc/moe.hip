@@ -552,38 +552,53 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t row_buffer(const uint16_t *p, 
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<uint16_t *>(p + (ok ? (size_t)r * H : 0)), 0,
                                            ok ? H * 2 : 0, 0x00020000);
 }
-constexpr int NT = 2;  // non-temporal
-template <int V>
-__device__ __forceinline__ u32x4 load_piece(__amdgpu_buffer_rsrc_t r, uint32_t off, bool nt) {
-  if (V == 1) return u32x4{(uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off, 0, 0), 0, 0, 0};
-  return __builtin_bit_cast(u32x4, nt ? __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, NT)
-                                      : __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+// A lane's piece: 8 elements (16 bytes) at byte `off` of a row of H.  TAIL: H is
+// not a multiple of 8, so rows start at any even address (the 16-byte accesses
+// need no more) and the last piece is short: its lane takes its elements one by
+// one.
+constexpr uint32_t NO = 0x80000000u;  // past any row: zeros, or nothing stored
+template <bool TAIL, bool NT>
+__device__ __forceinline__ u32x4 load_piece(__amdgpu_buffer_rsrc_t r, uint32_t off, int H) {
+  const bool whole = !TAIL || off + 16 <= (uint32_t)H * 2;
+  u32x4 v = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, whole ? off : NO, 0, NT ? 2 : 0));
+  if (TAIL && !whole && off < (uint32_t)H * 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t e = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(r, off + 2 * i, 0, 0);  // past the row: 0
+      v[i / 2] |= e << (16 * (i & 1));
+    }
+  }
+  return v;
 }
-template <int V>
-__device__ __forceinline__ void store_piece(__amdgpu_buffer_rsrc_t r, uint32_t off, u32x4 v) {
-  if (V == 1) __builtin_amdgcn_raw_buffer_store_b16((uint16_t)v[0], r, off, 0, 0);
-  else __builtin_amdgcn_raw_buffer_store_b128(v, r, off, 0, 0);
+template <bool TAIL>
+__device__ __forceinline__ void store_piece(__amdgpu_buffer_rsrc_t r, uint32_t off, int H, u32x4 v) {
+  const bool whole = !TAIL || off + 16 <= (uint32_t)H * 2;
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, whole ? off : NO, 0, 0);
+  if (TAIL && !whole && off < (uint32_t)H * 2) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      __builtin_amdgcn_raw_buffer_store_b16((uint16_t)(v[i / 2] >> (16 * (i & 1))), r, off + 2 * i, 0, 0);
+  }
 }
 // element i of a piece
-template <int V>
 __device__ __forceinline__ float piece_at(const u32x4 &v, int i) {
   return (i & 1) ? bf16_hi(v[i / 2]) : bf16_lo(v[i / 2]);
 }
 
-// V elements per thread: 8 (16 bytes) where H allows, else 1.  Plain stores: the
+// Plain stores: the
 // product that follows reads the rows (dispatch, product and combine together
 // were 1-2% slower with non-temporal ones, which alone save 14% at 4096 x 4096
 // tokens to 8 rows each).
-template <int V>
+template <bool TAIL>
 __global__ __launch_bounds__(ROW_THREADS) void dispatch_bf16_kernel(const uint16_t *X, const int32_t *row,
                                                                     uint16_t *A, int T, int H, int k,
                                                                     int rows, int pieces) {
   int t, piece;
   if (!token_piece(T, pieces, t, piece)) return;
-  const uint32_t off = (uint32_t)(piece * 64 + (threadIdx.x & 63)) * V * 2;  // past the row: dropped
-  const u32x4 v = load_piece<V>(row_buffer(X, t, T, H), off, false);
+  const uint32_t off = (uint32_t)(piece * 64 + (threadIdx.x & 63)) * 16;  // past the row: dropped
+  const u32x4 v = load_piece<TAIL, false>(row_buffer(X, t, T, H), off, H);
   const int32_t *rt = row + (size_t)t * k;
-  for (int j = 0; j < k; ++j) store_piece<V>(row_buffer(A, rt[j], rows, H), off, v);
+  for (int j = 0; j < k; ++j) store_piece<TAIL>(row_buffer(A, rt[j], rows, H), off, H, v);
 }
 
 // 16 elements per thread, 8 threads per 128-wide block: the block is quantised
@@ -631,54 +646,54 @@ __global__ __launch_bounds__(ROW_THREADS) void dispatch_fp8_kernel(const uint16_
 // out[t] = sum_j w_j Y[row_j] in fp32, j ascending.  Bound by reading Y: 4095 x
 // 4096 tokens from 8 rows each 55.7 us, 5.4 TB/s.  Y is not read again:
 // non-temporal loads (76 us without).  KB choices at a time.
-template <int V, int KB>
+template <bool TAIL, int KB>
 __global__ __launch_bounds__(ROW_THREADS) void combine_kernel(const uint16_t *Y, const int32_t *row,
                                                               const float *w, uint16_t *out, int T,
                                                               int H, int k, int M, int pieces) {
   int t, piece;
   if (!token_piece(T, pieces, t, piece)) return;
-  const uint32_t off = (uint32_t)(piece * 64 + (threadIdx.x & 63)) * V * 2;
+  const uint32_t off = (uint32_t)(piece * 64 + (threadIdx.x & 63)) * 16;
   const int32_t *rt = row + (size_t)t * k;
-  float acc[V];
+  float acc[8];
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[i] = 0.f;
+  for (int i = 0; i < 8; ++i) acc[i] = 0.f;
   for (int j0 = 0; j0 < k; j0 += KB) {
     u32x4 y[KB];
     float f[KB];
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
       const int r = j0 + j < k ? rt[j0 + j] : -1;
-      y[j] = load_piece<V>(row_buffer(Y, r, M, H), off, true);
+      y[j] = load_piece<TAIL, true>(row_buffer(Y, r, M, H), off, H);
       f[j] = r < 0 || r >= M ? 0.f : w ? w[(size_t)t * k + j0 + j] : 1.f;  // not the weight of a missing row
     }
 #pragma unroll
     for (int j = 0; j < KB; ++j)
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(f[j], piece_at<V>(y[j], i), acc[i]);
+      for (int i = 0; i < 8; ++i) acc[i] = __builtin_fmaf(f[j], piece_at(y[j], i), acc[i]);
   }
-  u32x4 o = {bf16_of(acc[0]), 0, 0, 0};
-  if (V == 8) {
+  u32x4 o;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = bf16_pair(acc[(2 * i) % V], acc[(2 * i + 1) % V]);
-  }
-  store_piece<V>(row_buffer(out, t, T, H), off, o);
+  for (int i = 0; i < 4; ++i) o[i] = bf16_pair(acc[2 * i], acc[2 * i + 1]);
+  store_piece<TAIL>(row_buffer(out, t, T, H), off, H, o);
 }
 
 // dY[row_j] = w_j dout, dw_j = dout . Y[row_j].  Bound by HBM: 4095 x 4096 tokens
 // with 8 rows each 121 us, 4.7 TB/s.
-// One workgroup per token.  KB choices at a time share one reading of dout;
-// their products with Y are summed per thread, then over the wave and, through
-// LDS, over the four waves in order.  Plain access: with non-temporal stores
-// this and the product that reads dY took 1-6% longer together.
-template <int V, int KB>
-__global__ __launch_bounds__(ROW_THREADS) void combine_backward_kernel(const uint16_t *dout,
-                                                                       const uint16_t *Y,
-                                                                       const int32_t *row, const float *w,
-                                                                       uint16_t *dY, float *dw, int T,
-                                                                       int H, int k, int M) {
-  __shared__ float s_dot[ROW_WAVES][KB];
+// One workgroup of WAVES waves per token.  KB choices at a time share one reading
+// of dout; their products with Y are summed per thread, then over the wave and,
+// through LDS, over the waves in order.  TAIL: the H % 8 elements behind the
+// whole pieces are taken one a lane.  Plain access: with non-temporal stores this
+// and the product that reads dY took 1-6% longer together.
+template <bool TAIL, int KB, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void combine_backward_kernel(const uint16_t *dout,
+                                                                      const uint16_t *Y,
+                                                                      const int32_t *row, const float *w,
+                                                                      uint16_t *dY, float *dw, int T,
+                                                                      int H, int k, int M) {
+  __shared__ float s_dot[WAVES][KB];
   const int x = blockIdx.x % 8, t = x * (T / 8) + min(x, T % 8) + blockIdx.x / 8;  // as token_piece
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const uint32_t whole = (uint32_t)(H / 8) * 16;  // bytes of a row in whole pieces
   const __amdgpu_buffer_rsrc_t rd = row_buffer(dout, t, T, H);
   for (int j0 = 0; j0 < k; j0 += KB) {
     float dot[KB], f[KB];
@@ -691,24 +706,35 @@ __global__ __launch_bounds__(ROW_THREADS) void combine_backward_kernel(const uin
       f[j] = j0 + j < k ? w[(size_t)t * k + j0 + j] : 0.f;
       dot[j] = 0.f;
     }
-    for (uint32_t off = threadIdx.x * V * 2; off < (uint32_t)H * 2; off += ROW_THREADS * V * 2) {
-      const u32x4 d = load_piece<V>(rd, off, false);
+    for (uint32_t off = threadIdx.x * 16; off < whole; off += WAVES * 64 * 16) {
+      const u32x4 d = load_piece<false, false>(rd, off, H);
       u32x4 y[KB];
 #pragma unroll
-      for (int j = 0; j < KB; ++j) y[j] = load_piece<V>(ry[j], off, false);
+      for (int j = 0; j < KB; ++j) y[j] = load_piece<false, false>(ry[j], off, H);
 #pragma unroll
       for (int j = 0; j < KB; ++j) {
-        u32x4 o = {bf16_of(f[j] * piece_at<V>(d, 0)), 0, 0, 0};
-        if (V == 8) {
+        u32x4 o;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = bf16_pair(f[j] * bf16_lo(d[i]), f[j] * bf16_hi(d[i]));
-        }
-        store_piece<V>(rg[j], off, o);
+        for (int i = 0; i < 4; ++i) o[i] = bf16_pair(f[j] * bf16_lo(d[i]), f[j] * bf16_hi(d[i]));
+        store_piece<false>(rg[j], off, H, o);
 #pragma unroll
-        for (int i = 0; i < V; ++i) dot[j] = __builtin_fmaf(piece_at<V>(d, i), piece_at<V>(y[j], i), dot[j]);
+        for (int i = 0; i < 8; ++i) dot[j] = __builtin_fmaf(piece_at(d, i), piece_at(y[j], i), dot[j]);
       }
     }
-    if (j0 > 0) __syncthreads();  // the group before has been read
+    if (TAIL && (int)threadIdx.x < H % 8) {
+      const uint32_t off = whole + threadIdx.x * 2;
+      const float d = __uint_as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rd, off, 0, 0) << 16);
+      float y[KB];
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+        y[j] = __uint_as_float((uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(ry[j], off, 0, 0) << 16);
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        __builtin_amdgcn_raw_buffer_store_b16((uint16_t)bf16_of(f[j] * d), rg[j], off, 0, 0);
+        dot[j] = __builtin_fmaf(d, y[j], dot[j]);
+      }
+    }
+    if (WAVES > 1 && j0 > 0) __syncthreads();  // the group before has been read
 #pragma unroll
     for (int j = 0; j < KB; ++j) {
       const float s = wave_sum(dot[j]);
@@ -718,10 +744,11 @@ __global__ __launch_bounds__(ROW_THREADS) void combine_backward_kernel(const uin
     if ((int)threadIdx.x < KB && j0 + (int)threadIdx.x < k) {
       float s = 0.f;
 #pragma unroll
-      for (int v = 0; v < ROW_WAVES; ++v) s += s_dot[v][threadIdx.x];
+      for (int v = 0; v < WAVES; ++v) s += s_dot[v][threadIdx.x];
       const int r = row[(size_t)t * k + j0 + threadIdx.x];
       dw[(size_t)t * k + j0 + threadIdx.x] = r < 0 || r >= M ? 0.f : s;
     }
+    if (WAVES == 1) __syncthreads();  // read before the next group's are written
   }
 }
 
@@ -737,14 +764,23 @@ int check_rows(const void *P, const void *Q, const int32_t *row, int T, int H, i
   return FP8GEMM_OK;
 }
 
-// pieces of a row for V elements a lane; false if the grid would be too large
-bool row_pieces(int T, int H, int V, int &pieces, dim3 &grid) {
-  pieces = (H + 64 * V - 1) / (64 * V);
+// pieces of a row for `per` elements a lane; false if the grid would be too large
+bool row_pieces(int T, int H, int per, int &pieces, dim3 &grid) {
+  pieces = (H + 64 * per - 1) / (64 * per);
   const long long waves = (long long)T * pieces;
   if (waves >= LIM - ROW_WAVES) return false;
   grid = dim3((unsigned)((waves + ROW_WAVES - 1) / ROW_WAVES));
   return true;
 }
+
+// f<H % 8 != 0, choices at a time, more...> for k choices of rows of H
+#define ROWS_PICK(f, ...)                                                                     \
+  (H % 8 == 0 ? (k <= 2   ? reinterpret_cast<const void *>(&f<false, 2 __VA_ARGS__>)          \
+                 : k <= 4 ? reinterpret_cast<const void *>(&f<false, 4 __VA_ARGS__>)          \
+                          : reinterpret_cast<const void *>(&f<false, 8 __VA_ARGS__>))         \
+              : (k <= 2   ? reinterpret_cast<const void *>(&f<true, 2 __VA_ARGS__>)           \
+                 : k <= 4 ? reinterpret_cast<const void *>(&f<true, 4 __VA_ARGS__>)           \
+                          : reinterpret_cast<const void *>(&f<true, 8 __VA_ARGS__>)))
 
 }  // namespace
 
@@ -799,13 +835,12 @@ int moe_dispatch_bf16(const void *X, const int32_t *row, void *A, int T, int H, 
   const int st = check_rows(X, M == 0 ? X : A, row, T, H, k, M, G);
   if (st != FP8GEMM_OK) return st < 0 ? FP8GEMM_OK : st;
   if (M == 0) return FP8GEMM_OK;  // no row to write
-  const bool vec = H % 8 == 0;
   int rows = M * G, pieces;
   dim3 grid;
-  if (!row_pieces(T, H, vec ? 8 : 1, pieces, grid)) return FP8GEMM_UNSUPPORTED_SHAPE;
+  if (!row_pieces(T, H, 8, pieces, grid)) return FP8GEMM_UNSUPPORTED_SHAPE;
   void *args[] = {&X, &row, &A, &T, &H, &k, &rows, &pieces};
-  return launch(vec ? reinterpret_cast<const void *>(&dispatch_bf16_kernel<8>)
-                    : reinterpret_cast<const void *>(&dispatch_bf16_kernel<1>),
+  return launch(H % 8 == 0 ? reinterpret_cast<const void *>(&dispatch_bf16_kernel<false>)
+                           : reinterpret_cast<const void *>(&dispatch_bf16_kernel<true>),
                 grid, dim3(ROW_THREADS), args, stream);
 }
 
@@ -830,16 +865,11 @@ int moe_combine_bf16(const void *Y, const int32_t *row, const float *w, void *ou
   const int st = check_rows(M == 0 ? out : Y, out, row, T, H, k, M, 1);  // no row: Y is not read
   if (st != FP8GEMM_OK) return st < 0 ? FP8GEMM_OK : st;
   if (!aligned(w, 4)) return FP8GEMM_MISALIGNED;
-  const bool vec = H % 8 == 0;
   int pieces;
   dim3 grid;
-  if (!row_pieces(T, H, vec ? 8 : 1, pieces, grid)) return FP8GEMM_UNSUPPORTED_SHAPE;
+  if (!row_pieces(T, H, 8, pieces, grid)) return FP8GEMM_UNSUPPORTED_SHAPE;
   void *args[] = {&Y, &row, &w, &out, &T, &H, &k, &M, &pieces};
-  const void *f = !vec     ? reinterpret_cast<const void *>(&combine_kernel<1, 8>)
-                  : k <= 2 ? reinterpret_cast<const void *>(&combine_kernel<8, 2>)
-                  : k <= 4 ? reinterpret_cast<const void *>(&combine_kernel<8, 4>)
-                           : reinterpret_cast<const void *>(&combine_kernel<8, 8>);
-  return launch(f, grid, dim3(ROW_THREADS), args, stream);
+  return launch(ROWS_PICK(combine_kernel), grid, dim3(ROW_THREADS), args, stream);
 }
 
 int moe_combine_backward_bf16(const void *dout, const void *Y, const int32_t *row, const float *w,
@@ -853,11 +883,10 @@ int moe_combine_backward_bf16(const void *dout, const void *Y, const int32_t *ro
       !aligned(dw, 4))
     return FP8GEMM_MISALIGNED;
   void *args[] = {&dout, &Y, &row, &w, &dY, &dw, &T, &H, &k, &M};
-  const void *f = H % 8 != 0 ? reinterpret_cast<const void *>(&combine_backward_kernel<1, 8>)
-                  : k <= 2   ? reinterpret_cast<const void *>(&combine_backward_kernel<8, 2>)
-                  : k <= 4   ? reinterpret_cast<const void *>(&combine_backward_kernel<8, 4>)
-                             : reinterpret_cast<const void *>(&combine_backward_kernel<8, 8>);
-  return launch(f, dim3(T), dim3(ROW_THREADS), args, stream);
+  // short rows: one wave holds them in two rounds or fewer
+  const bool one = H <= 1024;
+  return launch(one ? ROWS_PICK(combine_backward_kernel, , 1) : ROWS_PICK(combine_backward_kernel, , 4),
+                dim3(T), dim3(one ? 64 : 256), args, stream);
 }
 
 }  // extern "C"
