@@ -47,40 +47,48 @@ __device__ __forceinline__ float weight_of(uint32_t key, float m) {
   return key == 0 ? 0.f : x == m ? 1.f : __expf(x - m);
 }
 
-// The keys of V consecutive logits of one token, from element e0 (those past E:
-// no choice); VEC: rows and e0 are whole 16-byte pieces
-template <int V, bool BF, bool VEC>
-__device__ __forceinline__ void load_keys(const void *logits, size_t row, int e0, int E, uint32_t (&key)[V]) {
-  if (VEC && (BF ? V % 8 : V % 4) == 0) {
-    constexpr int PER = BF ? 8 : 4;
+// How a token's E <= LANES V elements lie in its lanes: pieces of PER consecutive
+// ones (16 bytes where rows are whole pieces, VEC, else one element), dealt to
+// the lanes in turn, so a load or store of all lanes covers one run of memory.
+template <int LANES, int V, bool BF, bool VEC>
+struct Deal {
+  static constexpr int FULL = BF ? 8 : 4;
+  static constexpr int PER = VEC && V % FULL == 0 ? FULL : 1;
+  static __device__ __forceinline__ int at(int i, int l) { return (i / PER * LANES + l) * PER + i % PER; }
+};
+
+// The keys of lane l's elements of the token whose first element is `row` (those past E: no choice)
+template <int LANES, int V, bool BF, bool VEC>
+__device__ __forceinline__ void load_keys(const void *logits, size_t row, int l, int E, uint32_t (&key)[V]) {
+  using D = Deal<LANES, V, BF, VEC>;
 #pragma unroll
-    for (int p = 0; p < V / PER; ++p) {
+  for (int p = 0; p < V; p += D::PER) {
+    const int e = D::at(p, l);
+    const bool in = e < E;  // PER > 1: E is a multiple of it
+    if (D::PER > 1) {
       u32x4 v = {0, 0, 0, 0};
-      const bool in = e0 + p * PER < E;  // E is a multiple of PER
-      if (in) v = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(logits) + (row + e0 + p * PER) * (BF ? 2 : 4));
+      if (in) v = *reinterpret_cast<const u32x4 *>(static_cast<const uint8_t *>(logits) + (row + e) * (BF ? 2 : 4));
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
+      for (int i = 0; i < D::PER; ++i) {
         const float x = !BF ? __uint_as_float(v[i % 4]) : (i & 1) ? bf16_hi(v[i / 2 % 4]) : bf16_lo(v[i / 2 % 4]);
-        key[p * PER + i] = in ? key_of(x) : 0u;
+        key[p + i] = in ? key_of(x) : 0u;
       }
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
+    } else {
       float x = -__builtin_inff();
-      if (e0 + i < E)
-        x = BF ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(logits)[row + e0 + i] << 16)
-               : static_cast<const float *>(logits)[row + e0 + i];
-      key[i] = key_of(x);
+      if (in)
+        x = BF ? __uint_as_float((uint32_t)static_cast<const uint16_t *>(logits)[row + e] << 16)
+               : static_cast<const float *>(logits)[row + e];
+      key[p] = key_of(x);
     }
   }
 }
 
-// LANES lanes per token (64, or 16 with four tokens to a wave), V consecutive
-// logits per lane (E <= LANES V).  Each of the k rounds takes the greatest key,
-// the lowest index among equals, and clears it.
-//   64 lanes: the wave's greatest key is uniform; the first lane that holds it,
-//     and in that lane the first such element, is the lowest index.
+// LANES lanes per token (64, or 16 with four tokens to a wave), V logits per lane
+// (E <= LANES V).  Each of the k rounds takes the greatest key, the lowest index
+// among equals, and clears it.
+//   64 lanes: the wave's greatest key is uniform.  With one piece a lane the first
+//     lane that holds it, and in that lane the first such element, is the lowest
+//     index; with more, a second maximum finds it.
 //   16 lanes: the four tokens share every instruction, at a quarter of the
 //     instructions per token.  A bf16 key and the element's index fit one word,
 //     so one maximum finds both; an fp32 key takes a second one for the index.
@@ -94,8 +102,9 @@ __global__ __launch_bounds__(256) void topk_kernel(const void *logits, int32_t *
   const int l = threadIdx.x % LANES;
   const int t = blockIdx.x * TOKENS + threadIdx.x / LANES;
   if (LANES == 64 && t >= T) return;  // 16 lanes: a wave with a token keeps all of its lanes
+  using D = Deal<LANES, V, BF, VEC>;
   uint32_t key[V];
-  load_keys<V, BF, VEC>(logits, (size_t)min(t, T - 1) * E, l * V, E, key);
+  load_keys<LANES, V, BF, VEC>(logits, (size_t)min(t, T - 1) * E, l, E, key);
   float m = 0.f, sum = 0.f, mine = 0.f;
   int id = -1;
   if (!renorm) {
@@ -120,19 +129,21 @@ __global__ __launch_bounds__(256) void topk_kernel(const void *logits, int32_t *
       const uint32_t top = wave_max(best);
       if (top == 0) break;  // no choice is left
       if (j == 0) m = value_of(top);
-      const int from = __builtin_ctzll(__ballot(best == top));
+      int e;
+      if (D::PER == V) {
+        const int from = __builtin_ctzll(__ballot(best == top));
+        e = from * V + (int)lane_of(at, from);
+      } else {
+        e = 0xFFFF - (int)wave_max(best == top ? 0xFFFF - D::at(at, l) : 0);
+      }
       const float p = weight_of(top, m);
       if (renorm) sum += p;
-      const int e = from * V + (int)lane_of(at, from);
       if (l == j) {
         id = e;
         mine = p;
       }
-      if (l == from) {
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (i == at) key[i] = 0;
-      }
+      for (int i = 0; i < V; ++i) key[i] = D::at(i, l) == e ? 0u : key[i];
     }
   } else {
     // bf16: the key's low half is zero (all ones for negative values): the
@@ -140,7 +151,7 @@ __global__ __launch_bounds__(256) void topk_kernel(const void *logits, int32_t *
     if (BF) {
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (key[i]) key[i] = (key[i] & 0xFFFF0000u) | (uint32_t)(0xFFFF - (l * V + i));
+        if (key[i]) key[i] = (key[i] & 0xFFFF0000u) | (uint32_t)(0xFFFF - D::at(i, l));
     }
     for (int j = 0; j < k; ++j) {
       uint32_t best = 0;
@@ -156,10 +167,10 @@ __global__ __launch_bounds__(256) void topk_kernel(const void *logits, int32_t *
       } else {
         uint32_t low = 0;  // 0xFFFF - the lowest index that holds the key
 #pragma unroll
-        for (int i = V - 1; i >= 0; --i) low = key[i] == top ? (uint32_t)(0xFFFF - (l * V + i)) : low;
+        for (int i = V - 1; i >= 0; --i) low = key[i] == top ? (uint32_t)(0xFFFF - D::at(i, l)) : low;
         e = 0xFFFF - (int)row_max(low);
 #pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = l * V + i == e ? 0u : key[i];
+        for (int i = 0; i < V; ++i) key[i] = D::at(i, l) == e ? 0u : key[i];
       }
       if (top == 0) continue;  // none is left to this token
       const uint32_t value = !BF ? top : (top >> 31) ? top & 0xFFFF0000u : top | 0xFFFFu;
@@ -184,15 +195,15 @@ __device__ __forceinline__ uint32_t row_lane(uint32_t x) {
   return dpp<0x150 + J>(x);
 }
 
-template <int J, int V>
-__device__ __forceinline__ void add_choices(int k, int id, float g, int e0, float (&p)[V]) {
+template <int J, class D, int V>
+__device__ __forceinline__ void add_choices(int k, int id, float g, int l, float (&p)[V]) {
   if constexpr (J < 16) {
     if (J >= k) return;
-    const int e = (int)row_lane<J>((uint32_t)id) - e0;
+    const int e = (int)row_lane<J>((uint32_t)id);
     const float v = __uint_as_float(row_lane<J>(__float_as_uint(g)));
 #pragma unroll
-    for (int i = 0; i < V; ++i) p[i] += e == i ? v : 0.f;
-    add_choices<J + 1>(k, id, g, e0, p);
+    for (int i = 0; i < V; ++i) p[i] += e == D::at(i, l) ? v : 0.f;
+    add_choices<J + 1, D>(k, id, g, l, p);
   }
 }
 
@@ -207,6 +218,7 @@ __global__ __launch_bounds__(256) void topk_backward_kernel(const void *logits, 
                                                             void *dlogits, int T, int E, int k,
                                                             int renorm, float scale) {
   constexpr int TOKENS = 256 / LANES;
+  using D = Deal<LANES, V, BF, VEC>;
   const int l = threadIdx.x % LANES;
   const int t = blockIdx.x * TOKENS + threadIdx.x / LANES;
   if (LANES == 64 && t >= T) return;
@@ -229,7 +241,7 @@ __global__ __launch_bounds__(256) void topk_backward_kernel(const void *logits, 
   } else {
     g = wj * g;
     uint32_t key[V], best = 0;
-    load_keys<V, BF, VEC>(logits, (size_t)min(t, T - 1) * E, l * V, E, key);
+    load_keys<LANES, V, BF, VEC>(logits, (size_t)min(t, T - 1) * E, l, E, key);
 #pragma unroll
     for (int i = 0; i < V; ++i) best = max(best, key[i]);
     const float m = value_of(LANES == 64 ? wave_max(best) : row_max(best));
@@ -246,36 +258,32 @@ __global__ __launch_bounds__(256) void topk_backward_kernel(const void *logits, 
   }
   if constexpr (LANES == 64) {
     for (int j = 0; j < k; ++j) {
-      const int e = (int)lane_of((uint32_t)id, j) - l * V;
+      const int e = (int)lane_of((uint32_t)id, j);
       const float v = __uint_as_float(lane_of(__float_as_uint(g), j));
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (e == i) p[i] += v;
+        if (e == D::at(i, l)) p[i] += v;
     }
   } else {
-    add_choices<0>(k, id, g, l * V, p);
+    add_choices<0, D>(k, id, g, l, p);
   }
   if (t >= T) return;
-  const size_t at = (size_t)t * E + l * V;
-  if (VEC && (BF ? V % 8 : V % 4) == 0) {
-    constexpr int PER = BF ? 8 : 4;
 #pragma unroll
-    for (int q = 0; q < V / PER; ++q) {
-      if (l * V + q * PER >= E) break;
+  for (int q = 0; q < V; q += D::PER) {
+    const int e = D::at(q, l);
+    if (e >= E) break;
+    const size_t at = (size_t)t * E + e;
+    if (D::PER > 1) {
       u32x4 o;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        o[i] = BF ? bf16_pair(p[(q * PER + 2 * i) % V], p[(q * PER + 2 * i + 1) % V])
-                  : __float_as_uint(p[(q * PER + i) % V]);
-      *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(dlogits) + (at + q * PER) * (BF ? 2 : 4)) = o;
+        o[i] = BF ? bf16_pair(p[(q + 2 * i) % V], p[(q + 2 * i + 1) % V]) : __float_as_uint(p[(q + i) % V]);
+      *reinterpret_cast<u32x4 *>(static_cast<uint8_t *>(dlogits) + at * (BF ? 2 : 4)) = o;
+    } else if (BF) {
+      static_cast<uint16_t *>(dlogits)[at] = (uint16_t)bf16_of(p[q]);
+    } else {
+      static_cast<float *>(dlogits)[at] = p[q];
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (l * V + i < E) {
-        if (BF) static_cast<uint16_t *>(dlogits)[at + i] = (uint16_t)bf16_of(p[i]);
-        else static_cast<float *>(dlogits)[at + i] = p[i];
-      }
   }
 }
 
