@@ -78,7 +78,25 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *planes, i
   const int m = blockIdx.y, n0 = (blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6)) * B * 64;
   if (n0 >= N) return;
   const int ad = ids[m];
-  float v[B];  // column n0 + b 64 + p COLS + g
+  // the planes' values of column n0 + b 64 + p COLS + g, PL planes at a time; the
+  // first are asked for before the factors
+  constexpr int PL = 4;
+  const uint32_t plane = (uint32_t)M * N * 4;
+  const __amdgpu_buffer_rsrc_t rp = rsrc(planes, plane * n_planes);
+  float q[PL][B], d[B];
+  auto ask = [&](int i0) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i)
+#pragma unroll
+      for (int b = 0; b < B; ++b) {
+        const int n = n0 + b * 64 + p * COLS + g;
+        const bool in = i0 + i < n_planes && n < N;
+        q[i][b] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                                                rp, in ? (i0 + i) * plane + ((uint32_t)m * N + n) * 4 : OOB, 0, 0));
+      }
+  };
+  ask(0);
+  float v[B];  // h Lb^T of that column
 #pragma unroll
   for (int b = 0; b < B; ++b) v[b] = 0.f;
   if (ad >= 0 && ad < G) {
@@ -117,19 +135,18 @@ __global__ __launch_bounds__(256) void lora_expand_kernel(const float *planes, i
         }
     }
   }
-  const size_t plane = (size_t)M * N;
-  float d[B];
 #pragma unroll
-  for (int b = 0; b < B; ++b) {
-    const int n = n0 + b * 64 + p * COLS + g;
-    d[b] = n < N ? planes[(size_t)m * N + n] : 0.f;
+  for (int b = 0; b < B; ++b) d[b] = q[0][b];
+  for (int i0 = 0;;) {
+#pragma unroll
+    for (int i = 0; i < PL; ++i)
+#pragma unroll
+      for (int b = 0; b < B; ++b)
+        if (i0 + i > 0) d[b] += q[i][b];  // past the last plane: zeros
+    i0 += PL;
+    if (i0 >= n_planes) break;
+    ask(i0);
   }
-  for (int i = 1; i < n_planes; ++i)
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int n = n0 + b * 64 + p * COLS + g;
-      if (n < N) d[b] += planes[i * plane + (size_t)m * N + n];
-    }
 #pragma unroll
   for (int b = 0; b < B; ++b) {
     const int n = n0 + b * 64 + p * COLS + g;
