@@ -76,7 +76,7 @@ int moe_topk_backward_bf16(const void *logits, const int32_t *ids, const float *
  * ws: moe_sort_workspace(S, G) int32 of the caller's, contents arbitrary, free
  * again when the call's work is done (may be NULL when that is 0).
  * Constraints: S >= 0, 1 <= G <= 1024, M >= 0; S + 127 G (masked: S + G M)
- * below 2^31 - 4096; pointers 4-byte aligned.
+ * below 2^31 - 65536; pointers 4-byte aligned.
  */
 int moe_contiguous_rows(int S, int G);
 int moe_sort_workspace(int S, int G);

@@ -393,7 +393,7 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_place_kernel(const int32_t 
   __shared__ int s_wave[SORT_WAVES];
   constexpr int UNROLL = 8;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int s0 = blockIdx.x * CHUNK + wave * PER_WAVE;
+  const int s0 = (chunks > 1 ? blockIdx.x * CHUNK : 0) + wave * PER_WAVE;
   int id[PER_WAVE / 64];
 #pragma unroll
   for (int i = 0; i < PER_WAVE / 64; ++i) {
@@ -482,6 +482,7 @@ __global__ __launch_bounds__(SORT_THREADS) void sort_place_kernel(const int32_t 
     for (long long r = (long long)s_first[G] + blockIdx.x * SORT_THREADS + tid; r < M;
          r += (long long)gridDim.x * SORT_THREADS)
       m_indices[r] = -1;
+    if ((int)blockIdx.x >= chunks) return;  // there for the padding only
   }
 #pragma unroll
   for (int i = 0; i < PER_WAVE / 64; ++i) {
@@ -513,7 +514,7 @@ int sort(const int32_t *ids, int32_t *row, int32_t *m_indices, int32_t *counts, 
   if (S < 0 || G < 1 || M < 0) return FP8GEMM_INVALID_ARG;
   if (G > MAX_G) return FP8GEMM_UNSUPPORTED_SHAPE;
   // every row number that the kernel forms, dropped ones included, fits an int
-  const long long top = (masked ? (long long)G * M : 127LL * G) + S + CHUNK;
+  const long long top = (masked ? (long long)G * M : 127LL * G) + S + 16 * CHUNK;
   if (top >= LIM || (!masked && M % 128 != 0)) return FP8GEMM_UNSUPPORTED_SHAPE;
   if (!counts || (S > 0 && (!ids || !row)) || (!masked && M > 0 && !m_indices) ||
       (moe_sort_workspace(S, G) > 0 && !ws))
@@ -528,12 +529,16 @@ int sort(const int32_t *ids, int32_t *row, int32_t *m_indices, int32_t *counts, 
                           dim3(SORT_THREADS), args, stream);
     if (st != FP8GEMM_OK) return st;
   }
+  // contiguous layout: more workgroups share the padding (512 choices over 256
+  // experts, 33 000 rows: 7.9 us with one, 5.4 with 16; with one chunk they count
+  // its choices too)
+  const int grid = masked ? chunks : std::max(chunks, std::min(16, M / 2048));
   int g_bits = 0;  // of an expert's number
   while ((1 << g_bits) < G) ++g_bits;
   void *args[] = {&ids, &row, &m_indices, &counts, &ws, &S, &G, &M, &chunks, &g_bits};
   return launch(masked ? reinterpret_cast<const void *>(&sort_place_kernel<true>)
                        : reinterpret_cast<const void *>(&sort_place_kernel<false>),
-                dim3(chunks), dim3(SORT_THREADS), args, stream);
+                dim3(grid), dim3(SORT_THREADS), args, stream);
 }
 
 // ---- tokens to rows and back -----------------------------------------------
