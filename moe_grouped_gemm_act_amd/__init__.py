@@ -21,6 +21,10 @@ Example (one MoE layer's expert GEMMs on device tensors)::
 W13 holds each expert's [W_gate; W_up] rows (2I of them), W2 the down
 projection; s13 and s2 are their 128x128 block scales.  Every call enqueues
 on the current stream and may be captured into a HIP graph.
+
+The calls around them (the router's choice, the sort by expert, tokens to rows
+and back) and the products with low-rank adapters are bound in ``routed`` and
+are names of this package too.
 """
 from __future__ import annotations
 

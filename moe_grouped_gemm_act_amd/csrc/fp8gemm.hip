@@ -42,7 +42,8 @@
 // for long K, the walk visits the live tiles only, the experts listed by
 // load).  The fused SwiGLU + 1x128
 // requantisation epilogue and a BF16 variant without scales run on the same
-// kernels.
+// kernels, and so does the second factor of low-rank adapters beside a dense
+// product (lora.hip has the first).
 
 #include <hip/hip_runtime.h>
 #include <atomic>
@@ -603,6 +604,9 @@ __device__ __forceinline__ void store_bf16(const v4f (&acc)[TN][TM], uint16_t *D
 // is an out-of-range load: zeros, no traffic.  So every adapter's rows are read
 // once a weight tile whatever the order of the requests, and a tile pays
 // ceil(adapters lr / 64) blocks beside its K / 64 (BF16) or K / 128 (FP8).
+// Against the same kernel without: 4096 x 4096 x 7168 BF16, 12 requests of rank 64,
+// 199 and 194 us; 777 x 2112 x 7168 FP8, 5 of rank 32, 22.9 and 21.6 us; 4096 x 24576
+// x 1536 FP8, 12 of rank 64, 241 us (200 as the walk, which has no adapter blocks).
 //
 // LORA_BLOCKS is that.  LORA_DOTS (few rows): the launch holds, before the base
 // product's workgroups, others that form h by dot products at the same time;
